@@ -21,6 +21,7 @@
 
 #include "gad_attn.h"
 #include "gad_error.h"
+#include "gad_host.h"
 #include "gad_combine.cuh"
 #include "gad_kernels.cuh"
 #include "gad_oproj.cuh"
@@ -44,13 +45,9 @@ int gad_fail(int status, const char* fmt, ...) {
 
 namespace {
 
-#define fail gad_fail
+using namespace gad_host;
 
 constexpr int kMaxCtasPerSm = 2;
-constexpr int kMaxDevices = 64;
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // decode_kernel configuration for single-token steps: 128-key stages, 3 of
 // them, two CTAs per SM (so 128 KB of loads in flight per SM); each of the 4
@@ -109,90 +106,6 @@ WsLayout ws_layout(int B, int L, int ngrp, int sms) {
     off = align_up(off + (gad::META_INTS + NB) * 4);
     w.total = off;
     return w;
-}
-
-int current_device_sms(int* sms, int* major) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
-    e = cudaDeviceGetAttribute(major, cudaDevAttrComputeCapabilityMajor, dev);
-    if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
-    return GAD_OK;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// A driver entry point by name (nullptr if the driver does not export it).
-void* driver_fn(const char* name) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint(name, &f, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-        return nullptr;
-    return f;
-}
-
-// Unique id of the calling thread's current CUDA context, 0 if there is none
-// yet or the driver cannot say.  Per-device set-up done once (function
-// attributes, device-symbol addresses) is remembered together with this id,
-// so a new context on the device (after cudaDeviceReset, say) repeats it.
-unsigned long long current_ctx_id() {
-    static std::atomic<PFN_cuCtxGetCurrent_v4000> get_cur{nullptr};
-    static std::atomic<PFN_cuCtxGetId_v12000> get_id{nullptr};
-    PFN_cuCtxGetCurrent_v4000 gc = get_cur.load(std::memory_order_acquire);
-    PFN_cuCtxGetId_v12000 gi = get_id.load(std::memory_order_acquire);
-    if (gc == nullptr || gi == nullptr) {
-        gc = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(driver_fn("cuCtxGetCurrent"));
-        gi = reinterpret_cast<PFN_cuCtxGetId_v12000>(driver_fn("cuCtxGetId"));
-        if (gc == nullptr || gi == nullptr) return 0;
-        get_cur.store(gc, std::memory_order_release);
-        get_id.store(gi, std::memory_order_release);
-    }
-    CUcontext ctx = nullptr;
-    unsigned long long id = 0;
-    if (gc(&ctx) != CUDA_SUCCESS || ctx == nullptr || gi(ctx, &id) != CUDA_SUCCESS) return 0;
-    return id;
-}
-
-// One-time set-up per (device, context): `done[dev]` holds the id of the
-// context in which it last ran.
-struct OncePerContext {
-    std::atomic<unsigned long long> done[kMaxDevices];
-    bool is_done(int dev, unsigned long long ctx) const {
-        return ctx != 0 && done[dev].load(std::memory_order_acquire) == ctx;
-    }
-    void mark(int dev) { done[dev].store(current_ctx_id(), std::memory_order_release); }
-};
-
-// The current device index, checked against the per-device tables.
-int current_device(int* dev) {
-    cudaError_t e = cudaGetDevice(dev);
-    if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-    if (*dev < 0 || *dev >= kMaxDevices) return fail(GAD_ERR_DEVICE, "device index %d", *dev);
-    return GAD_OK;
-}
-
-cudaLaunchAttribute pdl_attr() {
-    cudaLaunchAttribute a;
-    std::memset(&a, 0, sizeof(a));
-    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a.val.programmaticStreamSerializationAllowed = 1;
-    return a;
-}
-
-// cuTensorMapEncodeTiled, looked up once through the runtime.
-int tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
-    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> encode{nullptr};
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encode.load(std::memory_order_acquire);
-    if (fn == nullptr) {
-        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(driver_fn("cuTensorMapEncodeTiled"));
-        if (fn == nullptr) return fail(GAD_ERR_CUDA, "cuTensorMapEncodeTiled entry point not found");
-        encode.store(fn, std::memory_order_release);
-    }
-    *out = fn;
-    return GAD_OK;
 }
 
 // A cache (K or V) as a 2D byte tensor of num_rows rows of row_bytes, read in

@@ -55,6 +55,12 @@ extern "C" {
 #define GAD_HIDDEN 8192    /* decoder hidden size: rows of the o-projection weight */
 #define GAD_MAX_OPROJ_T 262144 /* most tokens in one projection call */
 #define GAD_NOALLOC_SCRATCH_BYTES (16u << 20) /* built-in scratch of gad_attn_decode_noalloc */
+#define GAD_MAX_LINEAR (1 << 22)      /* largest extent of a linear layer's matrices */
+#define GAD_MAX_LINEAR_LD (1LL << 32) /* largest row stride of them, in values */
+#define GAD_MAX_BEAMS 64              /* most beams per request, most candidates kept */
+#define GAD_MAX_VOCAB (1 << 24)       /* largest vocabulary of a beam selection */
+#define GAD_MAX_CACHES 4096           /* most caches in one page copy */
+#define GAD_MAX_PAGE_BYTES (1 << 24)  /* largest page of a page copy */
 
 /* Return codes (0 = success). */
 typedef enum {
@@ -79,6 +85,9 @@ typedef enum {
  * the GPU.  The step's outputs are then not valid. */
 #define GAD_STATUS_ATTN_WAIT 1   /* an attention kernel gave up a wait */
 #define GAD_STATUS_OPROJ_WAIT 2  /* the output projection gave up a wait */
+#define GAD_STATUS_PAGES_POOL 4  /* a page operation found too few free pages */
+#define GAD_STATUS_PAGES_ROW 8   /* a request would outgrow its page-table row */
+#define GAD_STATUS_LINEAR_WAIT 16 /* a linear layer gave up a wait */
 
 /*
  * Bytes of device workspace that gad_attn_decode needs for B requests of L
@@ -334,7 +343,8 @@ typedef enum {
     GAD_DTYPE_U8 = 3,    /* bytes; accepted for the caches as E4M3 codes */
     GAD_DTYPE_I32 = 4,
     GAD_DTYPE_I64 = 5,
-    GAD_DTYPE_F32 = 6
+    GAD_DTYPE_F32 = 6,
+    GAD_DTYPE_F16 = 7
 } gad_dtype;
 
 /* A device tensor: data pointer, element type (gad_dtype), rank 1..4, extents
@@ -397,6 +407,199 @@ int gad_attn_decode_t(const gad_tensor* qkv, const gad_tensor* positions, const 
                       const gad_tensor* k_cache, const gad_tensor* v_cache,
                       const gad_tensor* k_scale, const gad_tensor* v_scale, int page_size,
                       int window, int use_rope, const gad_tensor* out, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Linear layer with epilogue                                                 */
+/* ------------------------------------------------------------------------- */
+
+/* Activations of gad_linear. */
+typedef enum {
+    GAD_ACT_NONE = 0,
+    GAD_ACT_RELU = 1,       /* max(v, 0)                                          */
+    GAD_ACT_GELU = 2,       /* v (1 + erf(v / sqrt 2)) / 2                        */
+    GAD_ACT_GELU_TANH = 3,  /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2    */
+    GAD_ACT_SILU = 4        /* v / (1 + exp(-v))                                  */
+} gad_activation;
+
+/*
+ * The linear layers around the attention step (projections, feed-forward
+ * matrices, vocabulary logits), any T, K and N:
+ *
+ *   y[t][n] = act(sum_k x[t][k] w[n][k] + bias[n]) + residual[t][n]
+ *
+ *   x         [T, K] of `dtype` (GAD_DTYPE_BF16 or GAD_DTYPE_F16), row t at
+ *             x + t * ldx; 16-byte aligned, ldx a multiple of 8 values, >= K
+ *   w         [N, K] of `dtype`, row n at w + n * ldw, as x
+ *   bias      [N] of `dtype`, or NULL
+ *   residual  [T, N] of `out_dtype`, rows ldr >= N values apart, or NULL
+ *   y         [T, N] of `out_dtype` (`dtype`, or GAD_DTYPE_F32), rows ldy >= N
+ *             apart, written; values between the rows are left as they were
+ *   T, K, N   1 to GAD_MAX_LINEAR each; row strides up to GAD_MAX_LINEAR_LD
+ *
+ * Sums and the epilogue are held in fp32, y is rounded once.  y may be the
+ * residual itself (same address and stride); any other overlap of y with the
+ * inputs is refused (GAD_ERR_UNSUPPORTED).  Results do not depend on timing.
+ * gad_oproj is the special case without an epilogue that chains to a step.
+ * Asynchronous on `stream`, allocates nothing; make the first call on a device
+ * before any stream capture on it.
+ */
+int gad_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* residual,
+               int64_t ldr, void* y, int64_t ldy, int T, int K, int N, int dtype, int out_dtype, int activation,
+               void* stream);
+
+/* Status of the linear layers on the current device, as gad_oproj_status:
+ * GAD_STATUS_LINEAR_WAIT if a call gave up a wait since the last read, then
+ * cleared. */
+int gad_linear_status(int* status, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Beam selection                                                             */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * One selection of beam search: for each of G requests the K best of all
+ * (beam, token) candidates.  Row g * W + w of logits belongs to beam w of
+ * request g, whose score so far is scores[g * W + w]:
+ *
+ *   score(w, v) = scores[w] + logits[w][v] - log(sum_u exp(logits[w][u]))
+ *
+ * and a finished beam has the one candidate (pad_token, scores[w]).
+ *
+ *   logits      [G W, V] of `dtype` (GAD_DTYPE_BF16, _F16 or _F32), rows
+ *               row_stride >= V values apart, aligned to the element size
+ *   scores      float32 [G W]; -infinity: a beam without candidates (at the
+ *               first step, all beams but one)
+ *   finished    uint8 [G W], nonzero for finished beams, or NULL
+ *   pad_token   the token of a finished beam's candidate, 0 <= pad_token < V
+ *   out_scores  float32 [G, K]: scores, best first
+ *   out_parent  int32 [G, K]: row (g * W + w) of the candidate's beam, as
+ *               gad_pages_fork takes it
+ *   out_token   int32 [G, K]: its token
+ *   W, K        1 to GAD_MAX_BEAMS (K may differ from W); V up to GAD_MAX_VOCAB;
+ *               G * W up to GAD_MAX_B
+ *   workspace   gad_beam_workspace_bytes(G, W, V, K) bytes, 256-byte aligned;
+ *               calls that overlap on the GPU need different ones
+ *
+ * Scores are compared in 64 bits and rounded to float32 on output; equal
+ * scores go to the lower w * V + v.  A logit of -infinity or NaN is never
+ * chosen; a beam whose logits hold a NaN or +infinity has no log-sum and thus
+ * no candidates.  Places that no candidate fills get score -infinity and
+ * parent and token -1.  Outputs may not overlap scores (GAD_ERR_UNSUPPORTED).
+ * Asynchronous on `stream`, allocates nothing, graph-capturable.
+ */
+int gad_beam_select(const void* logits, int dtype, int64_t row_stride, const float* scores, const uint8_t* finished,
+                    int pad_token, int G, int W, int V, int K, float* out_scores, int32_t* out_parent,
+                    int32_t* out_token, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of gad_beam_select (0 on bad arguments, with
+ * gad_last_error() set).  Host-only. */
+size_t gad_beam_workspace_bytes(int G, int W, int V, int K);
+
+/* ------------------------------------------------------------------------- */
+/* Page operations                                                            */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * The page tables that the attention step reads, over a reference-counted
+ * pool of pages.  The caller owns the state:
+ *
+ *   page_table  int32 [rows, max_pages]: row r's key i lies in page
+ *               page_table[r][i / page_size]
+ *   lens        int32 [rows]: tokens of row r; negative: no request (then no
+ *               entry of the row counts)
+ *   refs        int32 [num_pages], 16-byte aligned: how many table entries
+ *               hold the page; 0: the page is free
+ *
+ * Row r's first ceil(lens[r] / page_size) entries count; entries behind them
+ * are neither read nor written.  Full pages may be shared by any number of
+ * rows; a page that is only partly filled belongs to one row.  The page ids
+ * serve every layer: the caches themselves are copied by gad_pages_copy.
+ * Free pages are handed out lowest id first, in row order, so all results
+ * follow from the inputs alone.  Page ids outside [0, num_pages) are never
+ * followed.  page_size is 1 or 64, rows 1 to GAD_MAX_B.
+ *
+ * Calls run asynchronously on `stream`, allocate nothing and can be captured.
+ * The workspace (gad_pages_workspace_bytes, 256-byte aligned) needs no initial
+ * contents; calls that overlap on the GPU, or that share a pool, must not run
+ * at the same time.  Its first word is the call's status: GAD_STATUS_PAGES_*
+ * bits, read with gad_attn_step_status.
+ */
+size_t gad_pages_workspace_bytes(int rows, int64_t num_pages);
+
+/*
+ * Copies page src[i] to page dst[i], i < n (n may be 0), in every one of `caches` (HOST
+ * array of n_caches device pointers, 16-byte aligned, at most GAD_MAX_CACHES:
+ * the K and V caches of all layers), each num_pages pages of page_bytes (a
+ * multiple of 16, at most GAD_MAX_PAGE_BYTES).  Pairs with an id outside
+ * [0, num_pages) are skipped.  Contract: the dst pages differ from one another
+ * and from all src pages.
+ */
+int gad_pages_copy(void* const* caches, int n_caches, size_t page_bytes, int64_t num_pages, const int32_t* src,
+                   const int32_t* dst, int n, void* stream);
+
+/*
+ * Replaces rows_in rows by rows_out new ones (beam search's reordering, n
+ * samples of one prompt, dropping rows): new row r continues old row
+ * parent[r], or is empty for a parent outside [0, rows_in) or an empty one.
+ * Full pages are shared.  A partly filled last page goes to the first child
+ * (lowest r); every other child gets a fresh page, with the pair
+ * (copy_src[r], copy_dst[r]) for gad_pages_copy (-1, -1 where nothing is to be
+ * copied).  Pages that no row holds any more are free, and may be handed out
+ * by the same call.  If the pool has too few free pages, the last rows that
+ * need one keep their full pages only (out_lens is cut to a multiple of
+ * page_size) and GAD_STATUS_PAGES_POOL is set.
+ *
+ *   parent      int32 [rows_out]
+ *   out_table   int32 [rows_out, max_pages], out_lens int32 [rows_out]; they may
+ *               not overlap page_table and lens (GAD_ERR_UNSUPPORTED)
+ *   copy_src,   int32 [rows_out]
+ *   copy_dst
+ */
+int gad_pages_fork(const int32_t* page_table, const int32_t* lens, int rows_in, const int32_t* parent, int rows_out,
+                   int max_pages, int page_size, int32_t* refs, int64_t num_pages, int32_t* out_table,
+                   int32_t* out_lens, int32_t* copy_src, int32_t* copy_dst, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/*
+ * Makes room for L more tokens (1 to GAD_MAX_PREFILL_L) in every row that
+ * holds a request: hands out the pages, advances lens by L, and writes the
+ * positions and cache rows that the attention step takes:
+ *
+ *   positions   int64 [rows L]: lens[r] + j (the length before the call);
+ *               0 for empty rows
+ *   cache_loc   int64 [rows L]: the cache row of that position; -1 (a row that
+ *               the step never writes) for empty rows
+ *
+ * All or nothing: if the pool has too few free pages (GAD_STATUS_PAGES_POOL)
+ * or a row would need more than max_pages (GAD_STATUS_PAGES_ROW), the table,
+ * lens and refs stay as they are and every cache_loc is -1.
+ */
+int gad_pages_extend(int32_t* page_table, int32_t* lens, int rows, int L, int max_pages, int page_size, int32_t* refs,
+                     int64_t num_pages, int64_t* positions, int64_t* cache_loc, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * Releases the pages of the rows r with leave[r] != 0 (uint8 [rows]; NULL:
+ * all) and marks the rows empty (lens[r] = -1).
+ */
+int gad_pages_free(const int32_t* page_table, int32_t* lens, int rows, const uint8_t* leave, int max_pages,
+                   int page_size, int32_t* refs, int64_t num_pages, void* stream);
+
+/*
+ * Moves pages in use to the front of the pool: with U pages in use, the k-th
+ * one with an id >= U moves to the k-th free id below U, for k < max_moves
+ * (num_pages / 2 moves are always enough).  Rewrites the table's entries and
+ * refs, and lists the moves for gad_pages_copy:
+ *
+ *   copy_src,   int32 [max_moves]; -1 behind the last move
+ *   copy_dst
+ *   used        int32 [1]: U (after all moves every page in use is below it)
+ *
+ * The table must hold every row that shares the pool.
+ */
+int gad_pages_compact(int32_t* page_table, const int32_t* lens, int rows, int max_pages, int page_size, int32_t* refs,
+                      int64_t num_pages, int32_t* copy_src, int32_t* copy_dst, int max_moves, int32_t* used,
+                      void* workspace, size_t workspace_bytes, void* stream);
 
 /* Message for the last nonzero status returned on this host thread. */
 const char* gad_last_error(void);

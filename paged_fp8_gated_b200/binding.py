@@ -59,6 +59,31 @@ _lib.gad_attn_step_status.restype = ctypes.c_int
 _lib.gad_attn_step_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_int), _vp]
 _lib.gad_oproj_status.restype = ctypes.c_int
 _lib.gad_oproj_status.argtypes = [ctypes.POINTER(ctypes.c_int), _vp]
+_i64 = ctypes.c_int64
+_lib.gad_linear.restype = ctypes.c_int
+_lib.gad_linear.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64] + [ctypes.c_int] * 6 + [_vp]
+_lib.gad_linear_status.restype = ctypes.c_int
+_lib.gad_linear_status.argtypes = [ctypes.POINTER(ctypes.c_int), _vp]
+_lib.gad_beam_workspace_bytes.restype = ctypes.c_size_t
+_lib.gad_beam_workspace_bytes.argtypes = [ctypes.c_int] * 4
+_lib.gad_beam_select.restype = ctypes.c_int
+_lib.gad_beam_select.argtypes = ([_vp, ctypes.c_int, _i64, _vp, _vp] + [ctypes.c_int] * 5
+                                 + [_vp, _vp, _vp, _vp, ctypes.c_size_t, _vp])
+_lib.gad_pages_workspace_bytes.restype = ctypes.c_size_t
+_lib.gad_pages_workspace_bytes.argtypes = [ctypes.c_int, _i64]
+_lib.gad_pages_copy.restype = ctypes.c_int
+_lib.gad_pages_copy.argtypes = [_vp, ctypes.c_int, ctypes.c_size_t, _i64, _vp, _vp, ctypes.c_int, _vp]
+_lib.gad_pages_fork.restype = ctypes.c_int
+_lib.gad_pages_fork.argtypes = ([_vp, _vp, ctypes.c_int, _vp] + [ctypes.c_int] * 3 + [_vp, _i64]
+                                + [_vp] * 5 + [ctypes.c_size_t, _vp])
+_lib.gad_pages_extend.restype = ctypes.c_int
+_lib.gad_pages_extend.argtypes = ([_vp, _vp] + [ctypes.c_int] * 4 + [_vp, _i64]
+                                  + [_vp] * 3 + [ctypes.c_size_t, _vp])
+_lib.gad_pages_free.restype = ctypes.c_int
+_lib.gad_pages_free.argtypes = [_vp, _vp, ctypes.c_int, _vp, ctypes.c_int, ctypes.c_int, _vp, _i64, _vp]
+_lib.gad_pages_compact.restype = ctypes.c_int
+_lib.gad_pages_compact.argtypes = ([_vp, _vp] + [ctypes.c_int] * 3 + [_vp, _i64, _vp, _vp, ctypes.c_int]
+                                   + [_vp] * 2 + [ctypes.c_size_t, _vp])
 
 
 class GadTensor(ctypes.Structure):
@@ -90,14 +115,21 @@ EXPORTED = ("gad_attn_decode", "gad_attn_decode_heads", "gad_attn_decode_timed",
             "gad_attn_decode_noalloc", "gad_attn_workspace_bytes",
             "gad_attn_workspace_bytes_heads", "gad_last_error", "gad_status_string",
             "gad_attn_step_status", "gad_oproj_status", "gad_attn_set_workspace",
-            "gad_attn_workspace_bytes_t", "gad_attn_decode_t")
+            "gad_attn_workspace_bytes_t", "gad_attn_decode_t",
+            "gad_linear", "gad_linear_status", "gad_beam_select", "gad_beam_workspace_bytes",
+            "gad_pages_workspace_bytes", "gad_pages_copy", "gad_pages_fork", "gad_pages_extend",
+            "gad_pages_free", "gad_pages_compact")
 # gad_dtype codes (include/gad_attn.h)
-DTYPE_BF16, DTYPE_E4M3, DTYPE_U8, DTYPE_I32, DTYPE_I64, DTYPE_F32 = 1, 2, 3, 4, 5, 6
+DTYPE_BF16, DTYPE_E4M3, DTYPE_U8, DTYPE_I32, DTYPE_I64, DTYPE_F32, DTYPE_F16 = 1, 2, 3, 4, 5, 6, 7
 _DTYPE_CODES = {torch.bfloat16: DTYPE_BF16, torch.uint8: DTYPE_U8, torch.int32: DTYPE_I32,
-                torch.int64: DTYPE_I64, torch.float32: DTYPE_F32}
+                torch.int64: DTYPE_I64, torch.float32: DTYPE_F32, torch.float16: DTYPE_F16}
 if hasattr(torch, "float8_e4m3fn"):
     _DTYPE_CODES[torch.float8_e4m3fn] = DTYPE_E4M3
 NOALLOC_SCRATCH_BYTES = 16 << 20
+# gad_activation codes
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+# GAD_STATUS_* bits
+STATUS_ATTN_WAIT, STATUS_OPROJ_WAIT, STATUS_PAGES_POOL, STATUS_PAGES_ROW, STATUS_LINEAR_WAIT = 1, 2, 4, 8, 16
 
 
 class GadError(RuntimeError):
@@ -437,3 +469,307 @@ def attn_decode_t(qkv, positions, seq_lens, page_table, cache_loc, k_cache, v_ca
     if rc != 0:
         raise GadError(rc, "gad_attn_decode_t")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Linear layer, beam selection and page operations
+# ---------------------------------------------------------------------------
+
+class _on:
+    """Makes a tensor's device current for a call, and the stream one of that
+    device (a stream of another device is refused)."""
+
+    def __init__(self, dev: torch.device, stream: torch.cuda.Stream | None):
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
+        self.dev, self.stream, self.back = dev, stream, -1
+
+    def __enter__(self) -> int:
+        cur = torch.cuda.current_device()
+        if self.dev.index != cur:
+            self.back = cur
+            torch.cuda.set_device(self.dev)
+        return (self.stream or torch.cuda.current_stream(self.dev)).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.back >= 0:
+            torch.cuda.set_device(self.back)
+
+
+def _cuda(t, name: str, dev: torch.device, dtype, shape=None):
+    """A contiguous CUDA tensor of `dtype` (and `shape`) on `dev`."""
+    _need(t, name, dtype)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _rows(t, name: str, dev, dtype, shape):
+    """A matrix whose rows are contiguous; returns its row stride in values."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
+           residual: torch.Tensor | None = None, activation: str = "none",
+           out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+           stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """act(x @ w^T + bias) + residual through gad_linear.
+
+    x [T, K] and w [N, K] bf16 or fp16 (rows contiguous, a multiple of 8 values
+    apart); bias [N] of their type; residual and the result [T, N] of
+    ``out_dtype`` (that of x, or float32).  ``activation``: one of ACTIVATIONS.
+    ``out`` may be the residual itself.
+    """
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"x must be bfloat16 or float16, got {x.dtype}")
+    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("x and w must be matrices [T, K] and [N, K]")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    (T, K), N, dev = x.shape, w.shape[0], x.device
+    if out is not None:
+        out_dtype = out_dtype or out.dtype
+    elif out_dtype is None:
+        out_dtype = x.dtype
+    if out_dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"the result must be {x.dtype} or float32, got {out_dtype}")
+    ldx = _rows(x, "x", dev, x.dtype, (T, K))
+    ldw = _rows(w, "w", dev, x.dtype, (N, K))
+    if T == 1:
+        ldx = -(-ldx // 8) * 8          # the stride of a single row is never followed
+    if N == 1:
+        ldw = -(-ldw // 8) * 8
+    if bias is not None:
+        _cuda(bias, "bias", dev, x.dtype, (N,))
+    ldr = 0 if residual is None else _rows(residual, "residual", dev, out_dtype, (T, N))
+    if out is None:
+        out = torch.empty(T, N, dtype=out_dtype, device=dev)
+    ldy = _rows(out, "out", dev, out_dtype, (T, N))
+    with _on(dev, stream) as s:
+        st = _lib.gad_linear(x.data_ptr(), ldx, w.data_ptr(), ldw, None if bias is None else bias.data_ptr(),
+                             None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy,
+                             T, K, N, _DTYPE_CODES[x.dtype], _DTYPE_CODES[out_dtype], ACTIVATIONS[activation], s)
+    if st != 0:
+        raise GadError(st, "gad_linear")
+    return out
+
+
+def linear_status(stream: torch.cuda.Stream | None = None) -> int:
+    """GAD_STATUS_* bits of the linear layers since the last read (then cleared)."""
+    st = ctypes.c_int(-1)
+    s = stream or torch.cuda.current_stream()
+    with _on(s.device, s) as h:
+        rc = _lib.gad_linear_status(ctypes.byref(st), h)
+    if rc != 0:
+        raise GadError(rc, "gad_linear_status")
+    s.synchronize()
+    return int(st.value)
+
+
+def beam_workspace_bytes(G: int, W: int, V: int, K: int) -> int:
+    n = _lib.gad_beam_workspace_bytes(int(G), int(W), int(V), int(K))
+    if n == 0:
+        raise GadError(-2, "gad_beam_workspace_bytes")
+    return int(n)
+
+
+def alloc_beam_workspace(G: int, W: int, V: int, K: int, device=None) -> torch.Tensor:
+    """Scratch for beam_select with these sizes (256-byte aligned by torch's allocator)."""
+    return torch.empty(beam_workspace_bytes(G, W, V, K), dtype=torch.uint8, device=device or "cuda")
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, K: int, finished: torch.Tensor | None = None,
+                pad_token: int = 0, out: tuple | None = None, workspace: torch.Tensor | None = None,
+                stream: torch.cuda.Stream | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The K best (beam, token) candidates of every request through gad_beam_select.
+
+    logits [G, W, V] bf16, fp16 or float32 (each beam's row contiguous, rows evenly
+    apart); scores float32 [G, W]; finished uint8 or bool [G, W].  Returns scores
+    float32, parent rows int32 (as pages_fork takes them) and tokens int32, each [G, K].
+    """
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 3:
+        raise ValueError("logits must be a CUDA tensor [G, W, V]")
+    if logits.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
+    (G, W, V), dev = logits.shape, logits.device
+    ld = V if G * W <= 1 else logits.stride(1) if W > 1 else logits.stride(0)
+    if (V > 1 and logits.stride(2) != 1) or (G > 1 and W > 1 and logits.stride(0) != W * ld):
+        raise ValueError("logits must have contiguous rows that lie evenly apart")
+    _cuda(scores, "scores", dev, torch.float32, (G, W))
+    if finished is not None:
+        _cuda(finished, "finished", dev, torch.bool if finished.dtype == torch.bool else torch.uint8, (G, W))
+    if out is None:
+        out = (torch.empty(G, K, dtype=torch.float32, device=dev),
+               torch.empty(G, K, dtype=torch.int32, device=dev),
+               torch.empty(G, K, dtype=torch.int32, device=dev))
+    else:
+        for t, n, dt in zip(out, ("out scores", "out parent", "out token"),
+                            (torch.float32, torch.int32, torch.int32), strict=True):
+            _cuda(t, n, dev, dt, (G, K))
+    if workspace is None:
+        workspace = alloc_beam_workspace(G, W, V, K, dev)
+    else:
+        _cuda(workspace, "workspace", dev, torch.uint8)
+    with _on(dev, stream) as s:
+        st = _lib.gad_beam_select(logits.data_ptr(), _DTYPE_CODES[logits.dtype], ld, scores.data_ptr(),
+                                  None if finished is None else finished.data_ptr(), int(pad_token), G, W, V,
+                                  int(K), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
+                                  workspace.data_ptr(), workspace.numel(), s)
+    if st != 0:
+        raise GadError(st, "gad_beam_select")
+    return tuple(out)
+
+
+def pages_workspace_bytes(rows: int, num_pages: int) -> int:
+    n = _lib.gad_pages_workspace_bytes(int(rows), int(num_pages))
+    if n == 0:
+        raise GadError(-2, "gad_pages_workspace_bytes")
+    return int(n)
+
+
+def alloc_pages_workspace(rows: int, num_pages: int, device=None) -> torch.Tensor:
+    """Scratch for the page operations on a pool of num_pages; its first word is
+    their status (step_status)."""
+    return torch.empty(pages_workspace_bytes(rows, num_pages), dtype=torch.uint8, device=device or "cuda")
+
+
+def _pool(page_table, lens, refs):
+    """Checks the pool's state; returns (device, rows, max_pages, num_pages)."""
+    _need(page_table, "page_table", torch.int32, 2)
+    dev = page_table.device
+    _cuda(lens, "lens", dev, torch.int32, (page_table.shape[0],))
+    _need(refs, "refs", torch.int32, 1)
+    _cuda(refs, "refs", dev, torch.int32)
+    return dev, page_table.shape[0], page_table.shape[1], refs.numel()
+
+
+def _pages_ws(workspace, rows, num_pages, dev):
+    if workspace is None:
+        return alloc_pages_workspace(rows, num_pages, dev)
+    return _cuda(workspace, "workspace", dev, torch.uint8)
+
+
+def pages_copy(caches: list[torch.Tensor], src: torch.Tensor, dst: torch.Tensor,
+               stream: torch.cuda.Stream | None = None) -> None:
+    """Copies page src[i] to page dst[i] in every cache of the list (uint8 or E4M3
+    [num_pages, page_size, hkv, 64], all of one shape) through gad_pages_copy; pairs
+    with an id outside the pool (-1) are skipped."""
+    _need(src, "src", torch.int32, 1)
+    dev, n = src.device, src.numel()
+    _cuda(dst, "dst", dev, torch.int32, (n,))
+    if not caches:
+        raise ValueError("caches must hold at least one tensor")
+    shape = caches[0].shape
+    for i, c in enumerate(caches):
+        _cuda(c, f"caches[{i}]", dev, torch.uint8 if c.dtype != torch.float8_e4m3fn else c.dtype, shape)
+    num_pages = shape[0] if shape else 0
+    page_bytes = caches[0].numel() // num_pages if num_pages else 0
+    ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+    with _on(dev, stream) as s:
+        st = _lib.gad_pages_copy(ptrs, len(caches), page_bytes, num_pages, src.data_ptr(), dst.data_ptr(), n, s)
+    if st != 0:
+        raise GadError(st, "gad_pages_copy")
+
+
+def pages_fork(page_table: torch.Tensor, lens: torch.Tensor, parent: torch.Tensor, refs: torch.Tensor,
+               page_size: int, out: tuple | None = None, workspace: torch.Tensor | None = None,
+               stream: torch.cuda.Stream | None = None) -> tuple:
+    """New rows that continue the old rows ``parent`` (int32, any shape; -1: empty) through
+    gad_pages_fork.  Returns (page_table [n, max_pages], lens [n], copy_src [n], copy_dst [n]),
+    all int32; refs is updated in place.  Entries behind a row's last page are not written
+    (without ``out`` they are -1)."""
+    dev, rows, max_pages, num_pages = _pool(page_table, lens, refs)
+    _cuda(parent, "parent", dev, torch.int32)
+    n = parent.numel()
+    if out is None:
+        out = (torch.full((n, max_pages), -1, dtype=torch.int32, device=dev),
+               *(torch.empty(n, dtype=torch.int32, device=dev) for _ in range(3)))
+    else:
+        for t, name, shape in zip(out, ("out table", "out lens", "copy_src", "copy_dst"),
+                                  ((n, max_pages), (n,), (n,), (n,)), strict=True):
+            _cuda(t, name, dev, torch.int32, shape)
+    ws = _pages_ws(workspace, max(rows, n), num_pages, dev)
+    with _on(dev, stream) as s:
+        st = _lib.gad_pages_fork(page_table.data_ptr(), lens.data_ptr(), rows, parent.data_ptr(), n, max_pages,
+                                 int(page_size), refs.data_ptr(), num_pages, *(t.data_ptr() for t in out),
+                                 ws.data_ptr(), ws.numel(), s)
+    if st != 0:
+        raise GadError(st, "gad_pages_fork")
+    return tuple(out)
+
+
+def pages_extend(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int, L: int = 1,
+                 out: tuple | None = None, workspace: torch.Tensor | None = None,
+                 stream: torch.cuda.Stream | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Room for L more tokens in every row that holds a request, through gad_pages_extend:
+    page_table, lens and refs are updated in place; returns (positions, cache_loc) int64
+    [rows * L] as attn_decode takes them."""
+    dev, rows, max_pages, num_pages = _pool(page_table, lens, refs)
+    if out is None:
+        out = tuple(torch.empty(rows * max(int(L), 0), dtype=torch.int64, device=dev) for _ in range(2))
+    else:
+        for t, name in zip(out, ("positions", "cache_loc"), strict=True):
+            _cuda(t, name, dev, torch.int64, (rows * L,))
+    ws = _pages_ws(workspace, rows, num_pages, dev)
+    with _on(dev, stream) as s:
+        st = _lib.gad_pages_extend(page_table.data_ptr(), lens.data_ptr(), rows, int(L), max_pages, int(page_size),
+                                   refs.data_ptr(), num_pages, out[0].data_ptr(), out[1].data_ptr(),
+                                   ws.data_ptr(), ws.numel(), s)
+    if st != 0:
+        raise GadError(st, "gad_pages_extend")
+    return tuple(out)
+
+
+def pages_free(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int,
+               leave: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> None:
+    """Releases the pages of the rows with leave[r] != 0 (uint8 or bool; None: all rows) and
+    marks them empty, through gad_pages_free; lens and refs are updated in place."""
+    dev, rows, max_pages, num_pages = _pool(page_table, lens, refs)
+    if leave is not None:
+        _cuda(leave, "leave", dev, torch.bool if leave.dtype == torch.bool else torch.uint8, (rows,))
+    with _on(dev, stream) as s:
+        st = _lib.gad_pages_free(page_table.data_ptr(), lens.data_ptr(), rows,
+                                 None if leave is None else leave.data_ptr(), max_pages, int(page_size),
+                                 refs.data_ptr(), num_pages, s)
+    if st != 0:
+        raise GadError(st, "gad_pages_free")
+
+
+def pages_compact(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int,
+                  max_moves: int | None = None, out: tuple | None = None, workspace: torch.Tensor | None = None,
+                  stream: torch.cuda.Stream | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Moves pages in use to the front of the pool through gad_pages_compact: page_table and
+    refs are updated in place; returns (copy_src, copy_dst, used) int32 for pages_copy
+    (max_moves pairs, -1 behind the last; by default enough for any pool)."""
+    dev, rows, max_pages, num_pages = _pool(page_table, lens, refs)
+    if out is None:
+        m = max(1, num_pages // 2) if max_moves is None else int(max_moves)
+        out = (torch.empty(max(m, 0), dtype=torch.int32, device=dev),
+               torch.empty(max(m, 0), dtype=torch.int32, device=dev),
+               torch.empty(1, dtype=torch.int32, device=dev))
+    else:
+        m = out[0].numel() if max_moves is None else int(max_moves)
+        for t, name, shape in zip(out, ("copy_src", "copy_dst", "used"), ((m,), (m,), (1,)), strict=True):
+            _cuda(t, name, dev, torch.int32, shape)
+    ws = _pages_ws(workspace, rows, num_pages, dev)
+    with _on(dev, stream) as s:
+        st = _lib.gad_pages_compact(page_table.data_ptr(), lens.data_ptr(), rows, max_pages, int(page_size),
+                                    refs.data_ptr(), num_pages, out[0].data_ptr(), out[1].data_ptr(), m,
+                                    out[2].data_ptr(), ws.data_ptr(), ws.numel(), s)
+    if st != 0:
+        raise GadError(st, "gad_pages_compact")
+    return tuple(out)

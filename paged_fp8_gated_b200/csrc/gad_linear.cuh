@@ -1,0 +1,549 @@
+// gad_linear.cuh - the linear layer with its epilogue:
+//
+//   y = act(x w^T + bias) + residual
+//
+//   x [T, K], w [N, K] bf16 or fp16 (both the same), rows ldx / ldw apart;
+//   bias [N] of their type; residual and y [T, N] of y's type (x's or fp32),
+//   rows ldr / ldy apart.  fp32 accumulation, epilogue in fp32, one rounding.
+//
+// Two kernels, both with operands staged by TMA (128-byte swizzle, 64 values of
+// K a stage, anything outside the matrices read as zero), tcgen05 MMAs and
+// accumulators in tensor memory:
+//
+// linear_narrow_kernel: few tokens, bound by the stream of w.  D[n][t] with
+// the 128 weight rows as the MMA's M and up to 256 tokens as its N, one tile a
+// block.  A cluster of up to 8 blocks shares a tile's K range, so that there
+// are enough blocks to keep the loads of every SM in flight; their partial
+// sums meet in shared memory over the cluster, added in rank order (the result
+// does not depend on timing), and each block finishes a share of the tile.
+//
+// linear_wide_kernel: many tokens, bound by the tensor cores.  Persistent
+// pairs of blocks (cta_group::2), 256 x 256 tiles (each block holds 128 tokens
+// and 128 weight rows of a stage), two accumulators in tensor memory, so a
+// tile's epilogue runs beside the next tile's MMAs.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "gad_tc.cuh"
+
+namespace gad {
+namespace lin {
+
+constexpr int BK = 64;                       // K per stage: one 128-byte row
+constexpr int ROWS = 128;                    // weight rows (narrow), tokens or weight rows of a block (wide)
+constexpr int TILE = ROWS * BK * 2;          // bytes of 128 rows of a stage
+
+enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+enum Out { OUT_BF16 = 0, OUT_F16 = 1, OUT_F32 = 2 };
+
+struct Params {
+    const void* bias;        // of x's type, or null
+    const void* residual;    // of y's type, or null
+    void* y;
+    long long ldr, ldy;
+    int T, K, N;
+    int fp16;                // x, w and bias are fp16 (else bf16)
+    int out, act;            // Out, Act
+    int vec;                 // y (and residual) take aligned stores of four values
+    int tt, nstg;            // narrow: tokens per tile, ring stages
+    int mt, nt;              // wide: tiles along the tokens and along N
+    int* err;                // status word: STATUS_LINEAR_WAIT when a bounded wait gave up
+};
+constexpr int STATUS_LINEAR_WAIT = 16;
+
+__device__ __forceinline__ float load16(const void* p, size_t i, bool fp16) {
+    return fp16 ? __half2float(static_cast<const __half*>(p)[i])
+                : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// The activation over N values; `act` is uniform.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+    switch (act) {
+        case ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = v[i] > 0.f || v[i] != v[i] ? v[i] : 0.f;
+            break;
+        case ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
+            break;
+        case ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float u = 0.79788456080286536f * (v[i] + 0.044715f * v[i] * v[i] * v[i]);
+                v[i] = 0.5f * v[i] * (1.f + tanhf(u));
+            }
+            break;
+        case ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = v[i] / (1.f + expf(-v[i]));
+            break;
+        default: break;
+    }
+}
+
+// Residual and store of four values y[t][n .. n+3] (fewer at the row's end).
+__device__ __forceinline__ void store4(const Params& p, long long t, int n, const float (&v)[4]) {
+    const size_t at = t * p.ldy + n;
+    if (p.vec && n + 4 <= p.N) {
+        float r[4] = {v[0], v[1], v[2], v[3]};
+        if (p.out == OUT_F32) {
+            if (p.residual != nullptr) {
+                const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + t * p.ldr + n);
+                r[0] += q.x; r[1] += q.y; r[2] += q.z; r[3] += q.w;
+            }
+            *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = make_float4(r[0], r[1], r[2], r[3]);
+        } else if (p.out == OUT_BF16) {
+            if (p.residual != nullptr) {
+                const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + t * p.ldr + n);
+                r[0] += __uint_as_float(q.x << 16); r[1] += __uint_as_float(q.x & 0xffff0000u);
+                r[2] += __uint_as_float(q.y << 16); r[3] += __uint_as_float(q.y & 0xffff0000u);
+            }
+            __nv_bfloat162 a = __floats2bfloat162_rn(r[0], r[1]), b = __floats2bfloat162_rn(r[2], r[3]);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) =
+                make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+        } else {
+            if (p.residual != nullptr) {
+                const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const __half*>(p.residual) + t * p.ldr + n);
+                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&q.x));
+                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&q.y));
+                r[0] += a.x; r[1] += a.y; r[2] += b.x; r[3] += b.y;
+            }
+            *reinterpret_cast<uint2*>(static_cast<__half*>(p.y) + at) =
+                make_uint2(pack_f16x2(r[0], r[1]), pack_f16x2(r[2], r[3]));
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n + i >= p.N) break;
+        float r = v[i];
+        if (p.residual != nullptr)
+            r += p.out == OUT_F32 ? static_cast<const float*>(p.residual)[t * p.ldr + n + i]
+                                  : load16(p.residual, t * p.ldr + n + i, p.out == OUT_F16);
+        if (p.out == OUT_F32) static_cast<float*>(p.y)[at + i] = r;
+        else if (p.out == OUT_BF16) static_cast<__nv_bfloat16*>(p.y)[at + i] = __float2bfloat16(r);
+        else static_cast<__half*>(p.y)[at + i] = __float2half(r);
+    }
+}
+
+// ---- thread-block clusters ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// The address of `addr` (this block's shared memory) in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
+}
+
+// ---- tcgen05 on a pair of blocks (cta_group::2) ----
+__device__ __forceinline__ void tc2_alloc(uint32_t dst_smem, uint32_t ncols) {  // whole warp, in both blocks
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(dst_smem), "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tc2_relinquish() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void tc2_dealloc(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrives on `bar` in both blocks when the pair's MMAs issued so far are done.  Whole warp.
+__device__ __forceinline__ void tc2_commit_both(uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n .reg .b32 rx;\n elect.sync rx|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+// Four MMAs of K = 64: D (+)= A(a + 32 k bytes) B(b + 32 k bytes)^T, k = 0..3.  Whole warp, one lane issues.
+__device__ __forceinline__ void tc2_mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, e, t;\n .reg .b32 rx;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        " elect.sync rx|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " add.u64 a1, %1, 2;\n add.u64 a2, %1, 4;\n add.u64 a3, %1, 6;\n"
+        " add.u64 b1, %2, 2;\n add.u64 b2, %2, 4;\n add.u64 b3, %2, 6;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// TMA tile load into this block's shared memory whose bytes count on a barrier
+// of the pair's first block (`bar`: a cluster address).
+__device__ __forceinline__ void tma2_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const void* tmap) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+__device__ __forceinline__ uint32_t idesc(const Params& p, int m, int n) {
+    return p.fp16 ? idesc_f16_f32(m, n, 0) : idesc_bf16_f32(m, n, 0);
+}
+
+// ---- linear_narrow_kernel's shared memory ----
+constexpr int NARROW_THREADS = 128;
+constexpr int NARROW_MAX_STAGES = 12;
+constexpr int RED_PITCH = ROWS + 4;                       // floats per token of the partial sums
+__host__ __device__ constexpr int narrow_stage(int tt) { return TILE + tt * BK * 2; }
+__host__ __device__ constexpr int narrow_ring(int tt, int nstg) {  // ring, later the partial sums
+    const int ring = nstg * narrow_stage(tt), red = tt * RED_PITCH * 4;
+    return ring > red ? ring : red;
+}
+__host__ __device__ constexpr int narrow_smem(int tt, int nstg) {
+    return 1024 + narrow_ring(tt, nstg) + 8 * (2 * NARROW_MAX_STAGES + 1) + 8;
+}
+__host__ __device__ constexpr uint32_t narrow_cols(int tt) {
+    return tt <= 32 ? 32u : tt <= 64 ? 64u : tt <= 128 ? 128u : 256u;
+}
+
+// ---- linear_wide_kernel's shared memory ----
+constexpr int WIDE_STAGES = 5;
+constexpr int WIDE_EPI_WARPS = 8;
+constexpr int WIDE_THREADS = 32 * (4 + WIDE_EPI_WARPS);
+constexpr int WIDE_STAGE = 2 * TILE;                      // 128 tokens and 128 weight rows
+constexpr int WIDE_PITCH = 36;                            // floats per row of an epilogue warp's 32 x 32 values
+constexpr int WIDE_EPI = WIDE_EPI_WARPS * 32 * WIDE_PITCH * 4;
+constexpr int WIDE_BARS = 2 * WIDE_STAGES + 5;            // full, empty, 2 tile full, 2 tile empty, done
+constexpr int WIDE_SMEM = 1024 + WIDE_STAGES * WIDE_STAGE + WIDE_EPI + 8 * WIDE_BARS + 8;
+constexpr int WIDE_GROUP = 8;                             // token tiles that share a sweep over N
+
+}  // namespace lin
+
+__global__ void __launch_bounds__(lin::NARROW_THREADS)
+    linear_narrow_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
+                         const lin::Params p) {
+    using namespace lin;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    const int xs = p.tt * BK * 2, NSTG = p.nstg;
+    const uint32_t ring = smem_addr(smem);                 // [NSTG] weight rows, then [NSTG] token rows
+    const uint32_t xring = ring + NSTG * TILE;
+    uint8_t* ctrl = smem + narrow_ring(p.tt, NSTG);
+    const uint32_t bar0 = smem_addr(ctrl);
+    auto FULL = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(s); };
+    auto EMPTY = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(NSTG + s); };
+    const uint32_t DONE = bar0 + 8u * (2 * NARROW_MAX_STAGES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * NARROW_MAX_STAGES + 1));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 8 * (2 * NARROW_MAX_STAGES + 1) + 4);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int split = static_cast<int>(gridDim.x) / ((p.N + ROWS - 1) / ROWS);   // the cluster's blocks
+    const int rank = static_cast<int>(cluster_rank());
+    const int n0 = static_cast<int>(blockIdx.x) / split * ROWS, t0 = blockIdx.y * p.tt;
+    const int nk_all = (p.K + BK - 1) / BK;
+    const int k_first = static_cast<int>(static_cast<long long>(nk_all) * rank / split);
+    const int nk = static_cast<int>(static_cast<long long>(nk_all) * (rank + 1) / split) - k_first;
+    const uint32_t ncols = narrow_cols(p.tt);
+
+    if (tid == 0) {
+        tma_prefetch_map(&w_map);
+        tma_prefetch_map(&x_map);
+        for (int s = 0; s < NSTG; ++s) {
+            mbar_init(FULL(s), 1);
+            mbar_init(EMPTY(s), 1);
+        }
+        mbar_init(DONE, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        tc_alloc(smem_addr(tmem_slot), ncols);
+        tc_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait_primary();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t bytes = static_cast<uint32_t>(TILE + xs);
+            int issued = 0;
+            for (int kc = 0; kc < nk; ++kc) {
+                const int s = kc % NSTG;
+                if (kc >= NSTG && !wait_bounded(EMPTY(s), (kc / NSTG - 1) & 1, abort_flag)) break;
+                mbar_arrive_expect_tx(FULL(s), bytes);
+                tma_load_2d(ring + s * TILE, &w_map, (k_first + kc) * BK, n0, FULL(s));
+                tma_load_2d(xring + s * xs, &x_map, (k_first + kc) * BK, t0, FULL(s));
+                issued = kc + 1;
+            }
+            // every load has landed before the shared memory is used again
+            for (int kc = issued > NSTG ? issued - NSTG : 0; kc < issued; ++kc)
+                wait_bounded(FULL(kc % NSTG), (kc / NSTG) & 1, abort_flag, false, TEARDOWN_LIMIT_NS);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint32_t id = idesc(p, ROWS, p.tt);
+        for (int kc = 0; kc < nk; ++kc) {
+            const int s = kc % NSTG;
+            const bool got = wait_bounded(FULL(s), (kc / NSTG) & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) break;
+            tc_fence_after();
+            const uint32_t wa = ring + s * TILE, xa = xring + s * xs;
+            const uint64_t ad[4] = {smem_desc_sw128(wa), smem_desc_sw128(wa + 32), smem_desc_sw128(wa + 64),
+                                    smem_desc_sw128(wa + 96)};
+            const uint64_t bd[4] = {smem_desc_sw128(xa), smem_desc_sw128(xa + 32), smem_desc_sw128(xa + 64),
+                                    smem_desc_sw128(xa + 96)};
+            tc_mma_ss4(tmem, ad, bd, id, kc > 0 ? 1u : 0u);
+            tc_commit(EMPTY(s));
+        }
+        tc_commit(DONE);
+    }
+    const bool done = wait_bounded(DONE, 0, abort_flag, false, TEARDOWN_LIMIT_NS);
+    tc_fence_after();
+    __syncthreads();   // the loads have landed (warp 0) and the MMAs are done: the ring is free
+
+    // ---- partial sums to shared memory: red[t][n], lane = weight row ----
+    const int tn = p.T - t0 < p.tt ? p.T - t0 : p.tt;      // the tile's tokens
+    float* red = reinterpret_cast<float*>(smem);
+    if (__all_sync(0xffffffffu, done && !*abort_flag)) {
+        const uint32_t row = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+        uint32_t v[32];
+        for (int c0 = 0; c0 < tn; c0 += 32) {
+            tc_ld32(row + static_cast<uint32_t>(c0), v);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c0 + j < tn) red[(c0 + j) * RED_PITCH + 32 * warp + lane] = __uint_as_float(v[j]);
+        }
+    }
+    tc_fence_before();
+    cluster_sync();
+
+    // ---- this block's share of the tile: sum over the cluster, epilogue ----
+    {
+        const int items = tn * (ROWS / 4);
+        const int i0 = static_cast<int>(static_cast<long long>(items) * rank / split);
+        const int i1 = static_cast<int>(static_cast<long long>(items) * (rank + 1) / split);
+        for (int i = i0 + tid; i < i1; i += NARROW_THREADS) {
+            const int t = i / (ROWS / 4), c = i % (ROWS / 4) * 4, n = n0 + c;
+            if (n >= p.N) continue;
+            const uint32_t at = ring + static_cast<uint32_t>(t * RED_PITCH + c) * 4u;
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int s = 0; s < split; ++s) {
+                const float4 q = ld_cluster_f4(in_block(at, s));
+                v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
+            }
+            if (p.bias != nullptr) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (n + u < p.N) v[u] += load16(p.bias, n + u, p.fp16);
+            }
+            activate(v, p.act);
+            store4(p, t0 + t, n, v);
+        }
+    }
+    cluster_sync();   // the other blocks have read this one's sums
+    if (warp == 1) {
+        tc_fence_after();
+        tc_dealloc(tmem, ncols);
+    }
+    if (tid == 0 && *abort_flag) atomicOr(p.err, STATUS_LINEAR_WAIT);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::WIDE_THREADS, 1)
+    linear_wide_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
+                       const lin::Params p) {
+    using namespace lin;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    const uint32_t ring = smem_addr(smem);                 // [stage][128 tokens | 128 weight rows]
+    float* epi = reinterpret_cast<float*>(smem + WIDE_STAGES * WIDE_STAGE);
+    uint8_t* ctrl = smem + WIDE_STAGES * WIDE_STAGE + WIDE_EPI;
+    const uint32_t bar0 = smem_addr(ctrl);
+    auto FULL = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(s); };
+    auto EMPTY = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(WIDE_STAGES + s); };
+    auto TFULL = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(2 * WIDE_STAGES + b); };
+    auto TEMPTY = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(2 * WIDE_STAGES + 2 + b); };
+    const uint32_t DONE = bar0 + 8u * (2 * WIDE_STAGES + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * WIDE_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 8 * WIDE_BARS + 4);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_rank());
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int tiles = p.mt * p.nt;
+    const int nk = (p.K + BK - 1) / BK;
+
+    if (tid == 0) {
+        tma_prefetch_map(&w_map);
+        tma_prefetch_map(&x_map);
+        for (int s = 0; s < WIDE_STAGES; ++s) {
+            mbar_init(FULL(s), 1);    // used in the pair's first block: its expected bytes are both blocks'
+            mbar_init(EMPTY(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(TFULL(b), 1);
+            mbar_init(TEMPTY(b), 2 * WIDE_EPI_WARPS);
+        }
+        mbar_init(DONE, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 2) {
+        tc2_alloc(smem_addr(tmem_slot), 512);
+        tc2_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both blocks' barriers exist
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait_primary();
+
+    // tile -> (token tile, weight tile): WIDE_GROUP token tiles sweep N together,
+    // so the pairs at work at one time share rows of x and of w in L2
+    auto place = [&](int tile, int* m, int* n) {
+        const int per = WIDE_GROUP * p.nt, g = tile / per, in = tile - g * per;
+        const int gm = p.mt - g * WIDE_GROUP < WIDE_GROUP ? p.mt - g * WIDE_GROUP : WIDE_GROUP;
+        *m = g * WIDE_GROUP + in % gm;
+        *n = in / gm;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                int m, n;
+                place(tile, &m, &n);
+                const int y = m * 256 + rank * ROWS, z = n * 256 + rank * ROWS;
+                for (int kc = 0; kc < nk; ++kc, ++it) {
+                    const int s = it % WIDE_STAGES;
+                    if (it >= WIDE_STAGES && !wait_bounded(EMPTY(s), (it / WIDE_STAGES - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(FULL(s), 2 * WIDE_STAGE);
+                    const uint32_t full = in_block(FULL(s), 0);
+                    tma2_load_2d(ring + s * WIDE_STAGE, &x_map, kc * BK, y, full);
+                    tma2_load_2d(ring + s * WIDE_STAGE + TILE, &w_map, kc * BK, z, full);
+                }
+            }
+            // the loads in flight land before the pair leaves (on the first block's barriers)
+            if (rank == 0)
+                for (int i = it > WIDE_STAGES ? it - WIDE_STAGES : 0; i < it; ++i)
+                    wait_bounded(FULL(i % WIDE_STAGES), (i / WIDE_STAGES) & 1, abort_flag, false, TEARDOWN_LIMIT_NS);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint32_t id = idesc(p, 256, 256);
+            int it = 0, local = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs, ++local) {
+                const int b = local & 1;
+                if (local >= 2) {
+                    const bool got = wait_bounded(TEMPTY(b), (local / 2 - 1) & 1, abort_flag);
+                    ok = __all_sync(0xffffffffu, got);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                for (int kc = 0; kc < nk; ++kc, ++it) {
+                    const int s = it % WIDE_STAGES;
+                    const bool got = wait_bounded(FULL(s), (it / WIDE_STAGES) & 1, abort_flag);
+                    ok = __all_sync(0xffffffffu, got);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = ring + s * WIDE_STAGE;
+                    tc2_mma_ss4(tmem + 256u * b, smem_desc_sw128(a), smem_desc_sw128(a + TILE), id, kc > 0 ? 1u : 0u);
+                    tc2_commit_both(EMPTY(s));
+                }
+                if (ok) tc2_commit_both(TFULL(b));
+            }
+            tc2_commit_both(DONE);
+        }
+    } else if (warp >= 4) {
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        float* mine = epi + (warp - 4) * 32 * WIDE_PITCH;
+        int local = 0;
+        for (int tile = pair; tile < tiles; tile += pairs, ++local) {
+            const int b = local & 1;
+            const bool got = wait_bounded(TFULL(b), (local / 2) & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) break;
+            tc_fence_after();
+            int m, n;
+            place(tile, &m, &n);
+            const long long row0 = static_cast<long long>(m) * 256 + rank * ROWS + quad * 32;
+            const uint32_t src = tmem + 256u * b + 128u * half + (static_cast<uint32_t>(32 * quad) << 16);
+            for (int c = 0; c < 4; ++c) {   // 32 columns at a time
+                const int col0 = n * 256 + half * 128 + c * 32;
+                uint32_t raw[32];
+                tc_ld32(src + 32u * c, raw);
+                tc_wait_ld();
+                if (c == 3) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(in_block(TEMPTY(b), 0));
+                }
+                if (col0 >= p.N) continue;
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                if (p.bias != nullptr) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] += col0 + j < p.N ? load16(p.bias, col0 + j, p.fp16) : 0.f;
+                }
+                activate(v, p.act);
+                // lane = token to lanes along N: through shared memory
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<float4*>(mine + lane * WIDE_PITCH + j) =
+                        make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = i * 4 + (lane >> 3), j = (lane & 7) * 4;
+                    const float4 q = *reinterpret_cast<const float4*>(mine + r * WIDE_PITCH + j);
+                    const float o[4] = {q.x, q.y, q.z, q.w};
+                    if (row0 + r < p.T && col0 + j < p.N) store4(p, row0 + r, col0 + j, o);
+                }
+            }
+        }
+    }
+    // ---- teardown: the MMAs are done (both blocks see it), then tensor memory goes ----
+    wait_bounded(DONE, 0, abort_flag, false, TEARDOWN_LIMIT_NS);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 2) {
+        tc_fence_after();
+        tc2_dealloc(tmem, 512);
+    }
+    if (tid == 0 && *abort_flag) atomicOr(p.err, STATUS_LINEAR_WAIT);
+}
+
+}  // namespace gad

@@ -475,50 +475,63 @@ def attn_decode_t(qkv, positions, seq_lens, page_table, cache_loc, k_cache, v_ca
 # Linear layer, beam selection and page operations
 # ---------------------------------------------------------------------------
 
-class _on:
-    """Makes a tensor's device current for a call, and the stream one of that
-    device (a stream of another device is refused)."""
+def _call(fn, dev: torch.device, stream: torch.cuda.Stream | None, *args) -> None:
+    """Calls a C entry point with the tensors' device current, on ``stream`` (by default that
+    device's current one; a stream of another device is refused)."""
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
+    else:
+        s = stream.cuda_stream
+    if dev.index == torch._C._cuda_getDevice():
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != 0:
+        raise GadError(st, fn.__name__)
 
-    def __init__(self, dev: torch.device, stream: torch.cuda.Stream | None):
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
-        self.dev, self.stream, self.back = dev, stream, -1
 
-    def __enter__(self) -> int:
-        cur = torch.cuda.current_device()
-        if self.dev.index != cur:
-            self.back = cur
-            torch.cuda.set_device(self.dev)
-        return (self.stream or torch.cuda.current_stream(self.dev)).cuda_stream
+def _make(stream: torch.cuda.Stream | None, make):
+    """make(), a call that creates tensors, on the stream that will use them."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
 
-    def __exit__(self, *exc):
-        if self.back >= 0:
-            torch.cuda.set_device(self.back)
+
+def _dev_of(t, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
 
 
 def _cuda(t, name: str, dev: torch.device, dtype, shape=None):
     """A contiguous CUDA tensor of `dtype` (and `shape`) on `dev`."""
-    _need(t, name, dtype)
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        _need(t, name, dtype)
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t
 
 
 def _rows(t, name: str, dev, dtype, shape):
     """A matrix whose rows are contiguous; returns its row stride in values."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda or t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape):
+        if _dev_of(t, name) != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+    return ld if shape[0] > 1 else max(ld, shape[1])   # a single row's stride is never followed
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
@@ -532,39 +545,37 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
     ``out_dtype`` (that of x, or float32).  ``activation``: one of ACTIVATIONS.
     ``out`` may be the residual itself.
     """
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
+    dev = _dev_of(x, "x")
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"x must be bfloat16 or float16, got {x.dtype}")
     if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("x and w must be matrices [T, K] and [N, K]")
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
-    (T, K), N, dev = x.shape, w.shape[0], x.device
-    if out is not None:
-        out_dtype = out_dtype or out.dtype
-    elif out_dtype is None:
-        out_dtype = x.dtype
-    if out_dtype not in (x.dtype, torch.float32):
-        raise TypeError(f"the result must be {x.dtype} or float32, got {out_dtype}")
-    ldx = _rows(x, "x", dev, x.dtype, (T, K))
-    ldw = _rows(w, "w", dev, x.dtype, (N, K))
+    (T, K), N = x.shape, w.shape[0]
+    dt = x.dtype
+    if out_dtype is None:
+        out_dtype = dt if out is None else out.dtype
+    if out_dtype is not dt and out_dtype is not torch.float32:
+        raise TypeError(f"the result must be {dt} or float32, got {out_dtype}")
+    ldx = _rows(x, "x", dev, dt, (T, K))
+    ldw = _rows(w, "w", dev, dt, (N, K))
     if T == 1:
-        ldx = -(-ldx // 8) * 8          # the stride of a single row is never followed
+        ldx = -(-ldx // 8) * 8
     if N == 1:
         ldw = -(-ldw // 8) * 8
     if bias is not None:
-        _cuda(bias, "bias", dev, x.dtype, (N,))
-    ldr = 0 if residual is None else _rows(residual, "residual", dev, out_dtype, (T, N))
+        bias = _cuda(bias, "bias", dev, dt, (N,)).data_ptr()
+    ldr = 0
+    if residual is not None:
+        ldr = _rows(residual, "residual", dev, out_dtype, (T, N))
+        residual = residual.data_ptr()
     if out is None:
-        out = torch.empty(T, N, dtype=out_dtype, device=dev)
+        out = _make(stream, lambda: torch.empty(T, N, dtype=out_dtype, device=dev))
     ldy = _rows(out, "out", dev, out_dtype, (T, N))
-    with _on(dev, stream) as s:
-        st = _lib.gad_linear(x.data_ptr(), ldx, w.data_ptr(), ldw, None if bias is None else bias.data_ptr(),
-                             None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy,
-                             T, K, N, _DTYPE_CODES[x.dtype], _DTYPE_CODES[out_dtype], ACTIVATIONS[activation], s)
-    if st != 0:
-        raise GadError(st, "gad_linear")
+    _call(_lib.gad_linear, dev, stream, x.data_ptr(), ldx, w.data_ptr(), ldw, bias, residual, ldr,
+          out.data_ptr(), ldy, T, K, N, _DTYPE_CODES[dt], _DTYPE_CODES[out_dtype], act)
     return out
 
 
@@ -572,10 +583,7 @@ def linear_status(stream: torch.cuda.Stream | None = None) -> int:
     """GAD_STATUS_* bits of the linear layers since the last read (then cleared)."""
     st = ctypes.c_int(-1)
     s = stream or torch.cuda.current_stream()
-    with _on(s.device, s) as h:
-        rc = _lib.gad_linear_status(ctypes.byref(st), h)
-    if rc != 0:
-        raise GadError(rc, "gad_linear_status")
+    _call(_lib.gad_linear_status, s.device, s, ctypes.byref(st))
     s.synchronize()
     return int(st.value)
 
@@ -601,36 +609,34 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, K: int, finished: to
     apart); scores float32 [G, W]; finished uint8 or bool [G, W].  Returns scores
     float32, parent rows int32 (as pages_fork takes them) and tokens int32, each [G, K].
     """
-    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 3:
-        raise ValueError("logits must be a CUDA tensor [G, W, V]")
+    dev = _dev_of(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [G, W, V]")
     if logits.dtype not in (torch.bfloat16, torch.float16, torch.float32):
         raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
-    (G, W, V), dev = logits.shape, logits.device
-    ld = V if G * W <= 1 else logits.stride(1) if W > 1 else logits.stride(0)
-    if (V > 1 and logits.stride(2) != 1) or (G > 1 and W > 1 and logits.stride(0) != W * ld):
+    G, W, V = logits.shape
+    sg, sw, sv = logits.stride()
+    ld = V if G * W <= 1 else sw if W > 1 else sg
+    if (V > 1 and sv != 1) or (G > 1 and W > 1 and sg != W * ld):
         raise ValueError("logits must have contiguous rows that lie evenly apart")
     _cuda(scores, "scores", dev, torch.float32, (G, W))
     if finished is not None:
         _cuda(finished, "finished", dev, torch.bool if finished.dtype == torch.bool else torch.uint8, (G, W))
     if out is None:
-        out = (torch.empty(G, K, dtype=torch.float32, device=dev),
-               torch.empty(G, K, dtype=torch.int32, device=dev),
-               torch.empty(G, K, dtype=torch.int32, device=dev))
+        out = _make(stream, lambda: tuple(torch.empty(G, K, dtype=dt, device=dev)
+                                          for dt in (torch.float32, torch.int32, torch.int32)))
     else:
         for t, n, dt in zip(out, ("out scores", "out parent", "out token"),
                             (torch.float32, torch.int32, torch.int32), strict=True):
             _cuda(t, n, dev, dt, (G, K))
     if workspace is None:
-        workspace = alloc_beam_workspace(G, W, V, K, dev)
+        workspace = _make(stream, lambda: alloc_beam_workspace(G, W, V, K, dev))
     else:
         _cuda(workspace, "workspace", dev, torch.uint8)
-    with _on(dev, stream) as s:
-        st = _lib.gad_beam_select(logits.data_ptr(), _DTYPE_CODES[logits.dtype], ld, scores.data_ptr(),
-                                  None if finished is None else finished.data_ptr(), int(pad_token), G, W, V,
-                                  int(K), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
-                                  workspace.data_ptr(), workspace.numel(), s)
-    if st != 0:
-        raise GadError(st, "gad_beam_select")
+    _call(_lib.gad_beam_select, dev, stream, logits.data_ptr(), _DTYPE_CODES[logits.dtype], ld,
+          scores.data_ptr(), None if finished is None else finished.data_ptr(), int(pad_token), G, W, V,
+          int(K), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), workspace.data_ptr(),
+          workspace.numel())
     return tuple(out)
 
 
@@ -649,17 +655,18 @@ def alloc_pages_workspace(rows: int, num_pages: int, device=None) -> torch.Tenso
 
 def _pool(page_table, lens, refs):
     """Checks the pool's state; returns (device, rows, max_pages, num_pages)."""
-    _need(page_table, "page_table", torch.int32, 2)
-    dev = page_table.device
-    _cuda(lens, "lens", dev, torch.int32, (page_table.shape[0],))
-    _need(refs, "refs", torch.int32, 1)
-    _cuda(refs, "refs", dev, torch.int32)
-    return dev, page_table.shape[0], page_table.shape[1], refs.numel()
+    dev = _dev_of(page_table, "page_table")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [rows, max_pages], got {list(page_table.shape)}")
+    rows, max_pages = _cuda(page_table, "page_table", dev, torch.int32).shape
+    _cuda(lens, "lens", dev, torch.int32, (rows,))
+    num_pages = _cuda(refs, "refs", dev, torch.int32).numel()
+    return dev, rows, max_pages, num_pages
 
 
-def _pages_ws(workspace, rows, num_pages, dev):
+def _pages_ws(workspace, rows, num_pages, dev, stream):
     if workspace is None:
-        return alloc_pages_workspace(rows, num_pages, dev)
+        return _make(stream, lambda: alloc_pages_workspace(rows, num_pages, dev))
     return _cuda(workspace, "workspace", dev, torch.uint8)
 
 
@@ -668,8 +675,8 @@ def pages_copy(caches: list[torch.Tensor], src: torch.Tensor, dst: torch.Tensor,
     """Copies page src[i] to page dst[i] in every cache of the list (uint8 or E4M3
     [num_pages, page_size, hkv, 64], all of one shape) through gad_pages_copy; pairs
     with an id outside the pool (-1) are skipped."""
-    _need(src, "src", torch.int32, 1)
-    dev, n = src.device, src.numel()
+    dev, n = _dev_of(src, "src"), src.numel()
+    _cuda(src, "src", dev, torch.int32, (n,))
     _cuda(dst, "dst", dev, torch.int32, (n,))
     if not caches:
         raise ValueError("caches must hold at least one tensor")
@@ -679,10 +686,8 @@ def pages_copy(caches: list[torch.Tensor], src: torch.Tensor, dst: torch.Tensor,
     num_pages = shape[0] if shape else 0
     page_bytes = caches[0].numel() // num_pages if num_pages else 0
     ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
-    with _on(dev, stream) as s:
-        st = _lib.gad_pages_copy(ptrs, len(caches), page_bytes, num_pages, src.data_ptr(), dst.data_ptr(), n, s)
-    if st != 0:
-        raise GadError(st, "gad_pages_copy")
+    _call(_lib.gad_pages_copy, dev, stream, ptrs, len(caches), page_bytes, num_pages, src.data_ptr(),
+          dst.data_ptr(), n)
 
 
 def pages_fork(page_table: torch.Tensor, lens: torch.Tensor, parent: torch.Tensor, refs: torch.Tensor,
@@ -696,19 +701,16 @@ def pages_fork(page_table: torch.Tensor, lens: torch.Tensor, parent: torch.Tenso
     _cuda(parent, "parent", dev, torch.int32)
     n = parent.numel()
     if out is None:
-        out = (torch.full((n, max_pages), -1, dtype=torch.int32, device=dev),
-               *(torch.empty(n, dtype=torch.int32, device=dev) for _ in range(3)))
+        out = _make(stream, lambda: (torch.full((n, max_pages), -1, dtype=torch.int32, device=dev),
+                                     *(torch.empty(n, dtype=torch.int32, device=dev) for _ in range(3))))
     else:
         for t, name, shape in zip(out, ("out table", "out lens", "copy_src", "copy_dst"),
                                   ((n, max_pages), (n,), (n,), (n,)), strict=True):
             _cuda(t, name, dev, torch.int32, shape)
-    ws = _pages_ws(workspace, max(rows, n), num_pages, dev)
-    with _on(dev, stream) as s:
-        st = _lib.gad_pages_fork(page_table.data_ptr(), lens.data_ptr(), rows, parent.data_ptr(), n, max_pages,
-                                 int(page_size), refs.data_ptr(), num_pages, *(t.data_ptr() for t in out),
-                                 ws.data_ptr(), ws.numel(), s)
-    if st != 0:
-        raise GadError(st, "gad_pages_fork")
+    ws = _pages_ws(workspace, max(rows, n), num_pages, dev, stream)
+    _call(_lib.gad_pages_fork, dev, stream, page_table.data_ptr(), lens.data_ptr(), rows, parent.data_ptr(),
+          n, max_pages, int(page_size), refs.data_ptr(), num_pages, *(t.data_ptr() for t in out),
+          ws.data_ptr(), ws.numel())
     return tuple(out)
 
 
@@ -720,17 +722,15 @@ def pages_extend(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tenso
     [rows * L] as attn_decode takes them."""
     dev, rows, max_pages, num_pages = _pool(page_table, lens, refs)
     if out is None:
-        out = tuple(torch.empty(rows * max(int(L), 0), dtype=torch.int64, device=dev) for _ in range(2))
+        out = _make(stream, lambda: tuple(torch.empty(rows * max(int(L), 0), dtype=torch.int64, device=dev)
+                                          for _ in range(2)))
     else:
         for t, name in zip(out, ("positions", "cache_loc"), strict=True):
             _cuda(t, name, dev, torch.int64, (rows * L,))
-    ws = _pages_ws(workspace, rows, num_pages, dev)
-    with _on(dev, stream) as s:
-        st = _lib.gad_pages_extend(page_table.data_ptr(), lens.data_ptr(), rows, int(L), max_pages, int(page_size),
-                                   refs.data_ptr(), num_pages, out[0].data_ptr(), out[1].data_ptr(),
-                                   ws.data_ptr(), ws.numel(), s)
-    if st != 0:
-        raise GadError(st, "gad_pages_extend")
+    ws = _pages_ws(workspace, rows, num_pages, dev, stream)
+    _call(_lib.gad_pages_extend, dev, stream, page_table.data_ptr(), lens.data_ptr(), rows, int(L),
+          max_pages, int(page_size), refs.data_ptr(), num_pages, out[0].data_ptr(), out[1].data_ptr(),
+          ws.data_ptr(), ws.numel())
     return tuple(out)
 
 
@@ -741,12 +741,8 @@ def pages_free(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
     dev, rows, max_pages, num_pages = _pool(page_table, lens, refs)
     if leave is not None:
         _cuda(leave, "leave", dev, torch.bool if leave.dtype == torch.bool else torch.uint8, (rows,))
-    with _on(dev, stream) as s:
-        st = _lib.gad_pages_free(page_table.data_ptr(), lens.data_ptr(), rows,
-                                 None if leave is None else leave.data_ptr(), max_pages, int(page_size),
-                                 refs.data_ptr(), num_pages, s)
-    if st != 0:
-        raise GadError(st, "gad_pages_free")
+    _call(_lib.gad_pages_free, dev, stream, page_table.data_ptr(), lens.data_ptr(), rows, None if leave is
+          None else leave.data_ptr(), max_pages, int(page_size), refs.data_ptr(), num_pages)
 
 
 def pages_compact(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int,
@@ -758,18 +754,14 @@ def pages_compact(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tens
     dev, rows, max_pages, num_pages = _pool(page_table, lens, refs)
     if out is None:
         m = max(1, num_pages // 2) if max_moves is None else int(max_moves)
-        out = (torch.empty(max(m, 0), dtype=torch.int32, device=dev),
-               torch.empty(max(m, 0), dtype=torch.int32, device=dev),
-               torch.empty(1, dtype=torch.int32, device=dev))
+        out = _make(stream, lambda: tuple(torch.empty(max(n, 0), dtype=torch.int32, device=dev)
+                                          for n in (m, m, 1)))
     else:
         m = out[0].numel() if max_moves is None else int(max_moves)
         for t, name, shape in zip(out, ("copy_src", "copy_dst", "used"), ((m,), (m,), (1,)), strict=True):
             _cuda(t, name, dev, torch.int32, shape)
-    ws = _pages_ws(workspace, rows, num_pages, dev)
-    with _on(dev, stream) as s:
-        st = _lib.gad_pages_compact(page_table.data_ptr(), lens.data_ptr(), rows, max_pages, int(page_size),
-                                    refs.data_ptr(), num_pages, out[0].data_ptr(), out[1].data_ptr(), m,
-                                    out[2].data_ptr(), ws.data_ptr(), ws.numel(), s)
-    if st != 0:
-        raise GadError(st, "gad_pages_compact")
+    ws = _pages_ws(workspace, rows, num_pages, dev, stream)
+    _call(_lib.gad_pages_compact, dev, stream, page_table.data_ptr(), lens.data_ptr(), rows, max_pages,
+          int(page_size), refs.data_ptr(), num_pages, out[0].data_ptr(), out[1].data_ptr(), m,
+          out[2].data_ptr(), ws.data_ptr(), ws.numel())
     return tuple(out)

@@ -92,6 +92,19 @@ inline int current_device(int* dev) {
     return GAD_OK;
 }
 
+// Raises a kernel's dynamic shared-memory limit once per (device, context).
+inline int raise_smem(const void* kern, OncePerContext& once, int bytes) {
+    int dev = 0;
+    const int ds = current_device(&dev);
+    if (ds != GAD_OK) return ds;
+    if (!once.is_done(dev, current_ctx_id())) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        once.mark(dev);
+    }
+    return GAD_OK;
+}
+
 inline cudaLaunchAttribute pdl_attr() {
     cudaLaunchAttribute a;
     std::memset(&a, 0, sizeof(a));

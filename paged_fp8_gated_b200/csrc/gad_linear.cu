@@ -58,18 +58,6 @@ size_t extent(long long rows, long long ld, long long cols, int elem) {
     return static_cast<size_t>((rows - 1) * ld + cols) * elem;
 }
 
-int raise_smem(const void* kern, OncePerContext& once, int bytes) {
-    int dev = 0;
-    const int ds = current_device(&dev);
-    if (ds != GAD_OK) return ds;
-    if (!once.is_done(dev, current_ctx_id())) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        once.mark(dev);
-    }
-    return GAD_OK;
-}
-
 // Shared memory: 228 KB per SM, 1 KB of it the system's per block, 227 KB per
 // block at most.  Blocks of a cluster wait for one another, so all of them must
 // get their tensor memory (512 columns per SM) while others hold theirs: every

@@ -10,32 +10,27 @@ using namespace gad_host;
 
 namespace {
 
-// How a row is cut for beam_chunk_kernel: batches of four vectors per thread
-// (one when that leaves the GPU with few blocks), in as many segments as make
-// kBlocks blocks, the ones that 148 SMs hold at a time.
-constexpr int kLongNV = 4, kShortNV = 1;
-constexpr long long kBlocks = 148 * 4, kFewBlocks = 148 * 2;
+// How a row is cut for beam_chunk_kernel: into as many segments as make kBlocks
+// blocks, the ones that 148 SMs hold at a time, of NV vectors per thread.
+constexpr long long kBlocks = 148 * 4;
 
 struct Cut {
-    int nv, batch, S, B;
+    int S, NV;
 };
 Cut cut_rows(long long rows, int V, int elem) {
-    Cut c{};
-    const int vec = 16 / elem * gad::bm::THREADS;
-    const long long long_batches = (V + kLongNV * vec - 1) / (kLongNV * vec);
-    c.nv = rows * long_batches < kFewBlocks ? kShortNV : kLongNV;
-    c.batch = c.nv * vec;
-    const int batches = (V + c.batch - 1) / c.batch;
+    const int vec = 16 / elem * gad::bm::THREADS;   // elements in one vector of every thread
+    const int vectors = (V + vec - 1) / vec;
     long long S = kBlocks / rows;
     if (S < 1) S = 1;
-    if (S > batches) S = batches;
-    c.B = static_cast<int>((batches + S - 1) / S);
-    c.S = (batches + c.B - 1) / c.B;
+    if (S > vectors) S = vectors;
+    Cut c{};
+    c.NV = static_cast<int>((vectors + S - 1) / S);
+    c.S = (vectors + c.NV - 1) / c.NV;
     return c;
 }
 
 struct BeamWs {
-    size_t x_off, v_off, sum_off, total;
+    size_t cand_off, sum_off, total;
 };
 // For logits of either size: the larger of the two cuts.
 BeamWs beam_ws(long long rows, int V, int K) {
@@ -43,10 +38,8 @@ BeamWs beam_ws(long long rows, int V, int K) {
     const size_t parts = static_cast<size_t>(rows) * (s2 > s4 ? s2 : s4);
     BeamWs w{};
     size_t off = 0;
-    w.x_off = off;
-    off = align_up(off + parts * K * sizeof(float));
-    w.v_off = off;
-    off = align_up(off + parts * K * sizeof(int));
+    w.cand_off = off;
+    off = align_up(off + parts * K * sizeof(uint64_t));
     w.sum_off = off;
     off = align_up(off + parts * sizeof(float2));
     w.total = off;
@@ -62,21 +55,6 @@ int check_beam(int G, int W, int V, int K) {
     return GAD_OK;
 }
 static_assert(GAD_MAX_BEAMS == gad::bm::MAX_K, "the merge kernel's per-beam tables");
-
-struct Chunk {
-    void (*kern)(const gad::BeamParams);
-    int smem;
-    OncePerContext* raised;
-};
-template <class T, int NV>
-Chunk chunk_of() {
-    static OncePerContext raised;
-    return {gad::beam_chunk_kernel<T, NV>, gad::beam_smem<T, NV>(), &raised};
-}
-template <class T>
-Chunk chunk_kernel(int nv) {
-    return nv == kLongNV ? chunk_of<T, kLongNV>() : chunk_of<T, kShortNV>();
-}
 
 }  // namespace
 
@@ -129,31 +107,26 @@ int gad_beam_select(const void* logits, int dtype, int64_t row_stride, const flo
     p.K = K;
     const Cut cut = cut_rows(rows, V, dtype == GAD_DTYPE_F32 ? 4 : 2);
     p.S = cut.S;
-    p.B = cut.B;
+    p.NV = cut.NV;
     p.pad = pad_token;
-    p.cand_x = reinterpret_cast<float*>(ws + w.x_off);
-    p.cand_v = reinterpret_cast<int*>(ws + w.v_off);
+    p.cand = reinterpret_cast<uint64_t*>(ws + w.cand_off);
     p.sums = reinterpret_cast<float2*>(ws + w.sum_off);
     p.out_scores = out_scores;
     p.out_parent = out_parent;
     p.out_token = out_token;
 
-    const Chunk chunk = dtype == GAD_DTYPE_BF16  ? chunk_kernel<__nv_bfloat16>(cut.nv)
-                        : dtype == GAD_DTYPE_F16 ? chunk_kernel<__half>(cut.nv)
-                                                 : chunk_kernel<float>(cut.nv);
-    st = raise_smem(reinterpret_cast<const void*>(chunk.kern), *chunk.raised, chunk.smem);
-    if (st != GAD_OK) return st;
+    void (*kern)(const gad::BeamParams) = dtype == GAD_DTYPE_BF16  ? gad::beam_chunk_kernel<__nv_bfloat16>
+                                          : dtype == GAD_DTYPE_F16 ? gad::beam_chunk_kernel<__half>
+                                                                   : gad::beam_chunk_kernel<float>;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(static_cast<unsigned>(p.S), static_cast<unsigned>(rows));
     cfg.blockDim = dim3(gad::bm::THREADS);
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cfg.dynamicSmemBytes = chunk.smem;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, chunk.kern, p);
+    cudaError_t err = cudaLaunchKernelEx(&cfg, kern, p);
     if (err != cudaSuccess) return fail(GAD_ERR_CUDA, "beam chunk launch: %s", cudaGetErrorString(err));
     cudaLaunchAttribute attr = pdl_attr();
     cfg.gridDim = dim3(static_cast<unsigned>(G));
-    cfg.dynamicSmemBytes = 0;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     err = cudaLaunchKernelEx(&cfg, gad::beam_merge_kernel, p);

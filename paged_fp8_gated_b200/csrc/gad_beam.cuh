@@ -8,19 +8,20 @@
 // ties by the lower w V + v.
 //
 // The order within a beam is that of its logits, so one pass over the logits
-// suffices: each block takes a segment of a row, batch after batch through
-// registers, and leaves its K best logits, its maximum m and sum of exp(x - m)
-// (beam_chunk_kernel); a second kernel joins the segments' sums into lse_w and
-// ranks the W S K candidates (beam_merge_kernel).  The scores that decide the
-// order are held in 64 bits: candidates of different beams can be as close as
-// the last bits of lse_w.  A row's elements go to threads by their index,
-// whatever the row's alignment, so equal rows have equal sums and tie exactly.
+// suffices: each block takes a segment of a row and leaves its K best logits,
+// its maximum m and its sum of exp(x - m) (beam_chunk_kernel); a second kernel
+// joins the segments' sums into lse_w and ranks the W S K candidates
+// (beam_merge_kernel).  The scores that decide the order are held in 64 bits:
+// candidates of different beams can be as close as the last bits of lse_w.  A
+// row's elements go to threads by their index, whatever the row's alignment,
+// so equal rows have equal sums and tie exactly.
 //
-// The K best of a segment: the K-th largest of at least K group maxima of the
-// first batch is a lower bound of the K-th largest element, few elements reach
-// it, and ranking those by counting leaves the K best and a threshold that
-// later batches rarely pass.  If more than the buffer holds pass it (long
-// ties), the block takes the batch's K best one after another.
+// The K best of a segment: every thread streams its elements through registers
+// for its maximum and sum only, without a barrier.  The K-th largest of the
+// threads' maxima is a lower bound of the K-th largest element that about K
+// threads reach; their elements (K / 256 of the segment) are read again, and
+// the few that pass are ranked by counting.  If more than the buffer holds pass
+// (long ties), the block takes the K best one after another.
 //
 // Bound: one read of the logits; beside it one MUFU exponential per logit (16 a
 // cycle and SM: three quarters of the read's time for 16-bit logits) and about
@@ -40,7 +41,7 @@ constexpr int THREADS = 256;
 constexpr int MAX_K = 64;
 constexpr int BUF = 512;        // a segment's candidates that are ranked by counting
 constexpr int MERGE_BUF = 1024; // a request's
-constexpr int STAGES = 3;       // batches in shared memory: one in use, two on their way
+constexpr int GROUP = 4;        // vectors of a thread in flight
 constexpr float NEG_INF = -__builtin_huge_valf();
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -131,41 +132,29 @@ __device__ __forceinline__ float from_key(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// The K-th largest of the maxima of groups of threads (8 threads a group for
-// K <= 16, else 2), -inf if K groups have nothing: a lower bound of the K-th
-// largest element.  Each thread brings its own maximum.  All threads call it.
-__device__ __forceinline__ float group_threshold(float mine, int K, uint32_t* s_key, float* s_thr) {
-    const int tid = threadIdx.x;
-    uint32_t k = order_key(mine);
-    const int gs = K <= 16 ? 8 : 2;
-    k = max(k, __shfl_xor_sync(0xffffffffu, k, 1));
-    if (gs == 8) {
-        k = max(k, __shfl_xor_sync(0xffffffffu, k, 2));
-        k = max(k, __shfl_xor_sync(0xffffffffu, k, 4));
-    }
-    if (tid % gs == 0) s_key[tid / gs] = k;
-    __syncthreads();
-    if (tid < 32) {
-        uint32_t v[4];
-        const int per = THREADS / gs / 32;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = i < per ? s_key[tid + 32 * i] : 0u;
-        uint32_t top = 0;
-        for (int r = 0; r < K; ++r) {
-            const uint32_t m = max(max(v[0], v[1]), max(v[2], v[3]));
-            top = __reduce_max_sync(0xffffffffu, m);
-            const uint32_t who = __ballot_sync(0xffffffffu, m == top);
-            if (tid == __ffs(who) - 1) {   // takes one of its values out
-                if (v[0] == top) v[0] = 0;
-                else if (v[1] == top) v[1] = 0;
-                else if (v[2] == top) v[2] = 0;
-                else v[3] = 0;
-            }
+// A candidate as one number, larger is better: the value, then the lower index.
+// 0: none.
+__device__ __forceinline__ uint64_t pack(float x, uint32_t v) {
+    return static_cast<uint64_t>(order_key(x)) << 32 | (0xffffffffu - v);
+}
+__device__ __forceinline__ float value_of(uint64_t c) { return from_key(static_cast<uint32_t>(c >> 32)); }
+__device__ __forceinline__ uint32_t index_of(uint64_t c) { return 0xffffffffu - static_cast<uint32_t>(c); }
+
+// A value that at least K of the threads' keys reach, the largest there is or
+// one that exactly K reach: bisection over the key's bits, a counting barrier a
+// bit (about 16 of them; taking maxima out one by one costs 200 cycles each).
+// All threads call it; its first barrier also covers what they wrote before.
+__device__ __forceinline__ uint32_t kth_key(uint32_t key, int K) {
+    uint32_t t = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t up = t | 1u << bit;
+        const int c = __syncthreads_count(key >= up);
+        if (c >= K) {
+            t = up;
+            if (c == K) break;
         }
-        if (tid == 0) *s_thr = top == 0 ? NEG_INF : from_key(top);
     }
-    __syncthreads();
-    return *s_thr;
+    return t;
 }
 
 }  // namespace bm
@@ -176,212 +165,108 @@ struct BeamParams {
     const float* scores;      // [G W]
     const uint8_t* finished;  // [G W] or null
     int G, W, V, K;
-    int S, B;                 // S segments per row, of B batches
+    int S, NV;                // S segments per row, of NV vectors per thread
     int pad;
-    float* cand_x;            // [G W S K] the segments' best logits, best first (-inf: none)
-    int* cand_v;              // [G W S K] their tokens
+    uint64_t* cand;           // [G W S K] the segments' best logits and their tokens, best first (see pack)
     float2* sums;             // [G W S] maximum, sum of exp(x - maximum)
     float* out_scores;
     int *out_parent, *out_token;
 };
 
-// Rank of (x, v) among n entries: how many come before it.
-__device__ __forceinline__ int beam_rank(const float* xs, const int* vs, int n, float x, int v) {
+// How many of n candidates are better.
+__device__ __forceinline__ int beam_rank(const uint64_t* c, int n, uint64_t mine) {
     int rank = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-        const float e = xs[j];
-        rank += e > x || (e == x && vs[j] < v);
-    }
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) rank += c[j] > mine;
     return rank;
 }
 
-// One block per (segment, row).  A batch is NV vectors per thread: thread t
-// holds elements v0 + (i THREADS + t) VEC + u.  Batches arrive in shared memory
-// by cp.async, two ahead; a row that starts off a 16-byte boundary (by `mis`
-// bytes, the same for all its vectors) is copied from the boundary before it,
-// and an element vector is cut out of the two aligned ones that it lies in.
-template <class T, int NV>
+// 16 bytes of a row from element v on; elements past the row's end are -inf.  A
+// row that starts off a 16-byte boundary (by `mis` bytes, the same for all its
+// vectors) is read as the two aligned vectors that the elements lie in (the
+// second one comes from L1).
+template <class T>
+__device__ __forceinline__ void beam_load(uint32_t (&w)[4], const T* x, int v, int V, int mis) {
+    using E = bm::Elem<T>;
+    if (v >= V) {
+        w[0] = w[1] = w[2] = w[3] = E::LOWEST;
+        return;
+    }
+    const uint4* a = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x + v) - mis);
+    const uint4 lo = __ldg(a);
+    w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
+    if (mis != 0) {
+        // the second vector, unless the row ends in the first
+        const int in_first = (16 - mis) / static_cast<int>(sizeof(T));
+        const uint4 hi = v + in_first < V ? __ldg(a + 1) : make_uint4(0, 0, 0, 0);
+        uint32_t q[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        if (mis & 8) {
+#pragma unroll
+            for (int j = 0; j < 6; ++j) q[j] = q[j + 2];
+        }
+        if (mis & 4) {
+#pragma unroll
+            for (int j = 0; j < 5; ++j) q[j] = q[j + 1];
+        }
+        const int bits = 8 * (mis & 3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(q[j], q[j + 1], bits);
+    }
+    if (v + E::VEC > V) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = E::cut(w[j], V - v - j * (E::VEC / 4));
+    }
+}
+
+// One block per (segment, row).  Thread t holds the vectors i THREADS + t of
+// the segment, i < NV.
+template <class T>
 __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamParams p) {
     using namespace bm;
     using E = Elem<T>;
-    constexpr int VEC = E::VEC, BATCH = NV * VEC * THREADS, ESZ = static_cast<int>(sizeof(T));
-    constexpr int STAGE = BATCH * ESZ + 16;
-    extern __shared__ __align__(16) uint8_t ring[];   // [STAGES][STAGE]
-    __shared__ float s_m[THREADS / 32], s_thr;
+    constexpr int VEC = E::VEC;
+    __shared__ float s_m[THREADS / 32];
     __shared__ double s_sum[THREADS / 32];
-    __shared__ uint32_t s_key[128];
-    __shared__ float s_x[BUF], s_bx[MAX_K];
-    __shared__ int s_v[BUF], s_bv[MAX_K], s_new[3];
+    __shared__ uint64_t s_c[BUF];
+    __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, row = blockIdx.y;
     pdl_launch_dependents();
     {   // a finished beam's logits and those of a dead one are not needed
         const float s = p.scores[row];
         if ((p.finished != nullptr && p.finished[row] != 0) || !(s > NEG_INF)) return;
     }
-    if (tid < 3) s_new[tid] = 0;
+    if (tid == 0) s_n = 0;
     const T* x = static_cast<const T*>(p.logits) + row * p.ld;
     const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15);
-    const int first = static_cast<int>(static_cast<long long>(blockIdx.x) * p.B * BATCH);
-    const int left = (p.V - first + BATCH - 1) / BATCH, batches = left < p.B ? left : p.B;
-    const uint32_t ring_addr = smem_addr(ring);
-
-    // 16-byte pieces of batch b that hold elements of the row; the others become zero
-    const uint8_t* base = reinterpret_cast<const uint8_t*>(x) - mis;
-    const long long row_bytes = static_cast<long long>(p.V) * ESZ + mis;
-    auto fetch = [&](int b) {
-        if (b < batches) {
-            const long long at = (static_cast<long long>(first) + static_cast<long long>(b) * BATCH) * ESZ;
-            const uint32_t dst = ring_addr + static_cast<uint32_t>(b % STAGES) * STAGE;
+    const int first = static_cast<int>(static_cast<long long>(blockIdx.x) * p.NV * THREADS * VEC);
+    auto at = [&](int i, int t) { return first + (i * THREADS + t) * VEC; };   // below 2^25
+    auto load = [&](uint32_t (&w)[GROUP][4], int i0) {
+        if (mis == 0 && i0 + GROUP <= p.NV && at(i0 + GROUP, 0) <= p.V) {   // uniform: all of it inside
+            const uint4* a = reinterpret_cast<const uint4*>(x + at(i0, tid));
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int off = (i * THREADS + tid) * 16;
-                cp_async16(dst + off, at + off < row_bytes ? base + at + off : base, at + off < row_bytes ? 16 : 0);
+            for (int i = 0; i < GROUP; ++i) {
+                const uint4 q = __ldg(a + i * THREADS);
+                w[i][0] = q.x; w[i][1] = q.y; w[i][2] = q.z; w[i][3] = q.w;
             }
-            if (mis != 0 && tid == 0) {
-                const int off = BATCH * ESZ;
-                cp_async16(dst + off, at + off < row_bytes ? base + at + off : base, at + off < row_bytes ? 16 : 0);
-            }
-        }
-        cp_async_commit();
-    };
-    fetch(0);
-    fetch(1);
-
-    float m = NEG_INF, sum = 0.f;       // this thread's maximum and sum of exp(x - m)
-    float thr = NEG_INF;                // elements of the K best are above it (from the second batch on)
-    int held = 0;                       // entries of the buffer: at most 2 K + 15 between batches
-
-    // What batch b left in the buffer (all threads, after a barrier behind b's
-    // entries): cuts the buffer to its K best, best first, when it is long, for
-    // the first batch and at the end (`last`).
-    auto settle = [&](int b, bool last) {
-        const int fresh = s_new[b % 3];
-        if (fresh > BUF - held) {
-            // more than the buffer holds: the batch's K best one after another
-            const uint8_t* st = ring + (b % STAGES) * STAGE + mis;
-            const int v0 = first + b * BATCH;
-            float last_x = __builtin_huge_valf();
-            int last_v = -1;
-            for (int k = 0; k < p.K; ++k) {
-                float bx = NEG_INF;
-                int bv = 0x7fffffff;
-                for (int o = tid; o < BATCH && v0 + o < p.V; o += THREADS) {
-                    const float e = E::one(st + o * ESZ);
-                    const int v = v0 + o;
-                    const bool after = e < last_x || (e == last_x && v > last_v);
-                    if (after && e > NEG_INF && (e > bx || (e == bx && v < bv))) {
-                        bx = e;
-                        bv = v;
-                    }
-                }
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) {
-                    const float ox = __shfl_xor_sync(0xffffffffu, bx, d);
-                    const int ov = __shfl_xor_sync(0xffffffffu, bv, d);
-                    if (ox > bx || (ox == bx && ov < bv)) {
-                        bx = ox;
-                        bv = ov;
-                    }
-                }
-                __syncthreads();   // the last round's readers are done
-                if (lane == 0) {   // the buffer's end is scratch: what overflowed it is dropped
-                    s_x[BUF - 1 - (tid >> 5)] = bx;
-                    s_v[BUF - 1 - (tid >> 5)] = bv;
-                }
-                __syncthreads();
-                for (int w = 0; w < THREADS / 32; ++w) {
-                    const float ox = s_x[BUF - 1 - w];
-                    const int ov = s_v[BUF - 1 - w];
-                    if (ox > bx || (ox == bx && ov < bv)) {
-                        bx = ox;
-                        bv = ov;
-                    }
-                }
-                if (tid == 0) {
-                    s_x[held + k] = bx;
-                    s_v[held + k] = bv;
-                }
-                last_x = bx;
-                last_v = bv;
-            }
-            held += p.K;   // a batch that overflows the buffer has K elements above -inf
-            __syncthreads();
         } else {
-            held += fresh;
-        }
-        if (b == 0 || last || held >= 2 * p.K + 16) {
-            for (int i = tid; i < held; i += THREADS) {
-                const float e = s_x[i];
-                const int v = s_v[i], rank = beam_rank(s_x, s_v, held, e, v);
-                if (rank < p.K) {
-                    s_bx[rank] = e;
-                    s_bv[rank] = v;
-                }
-            }
-            __syncthreads();
-            if (held >= p.K) {
-                held = p.K;
-                thr = s_bx[p.K - 1];   // an equal element further on comes after it
-            } else {
-                thr = NEG_INF;
-            }
-            if (!last) {
-                for (int k = tid; k < held; k += THREADS) {
-                    s_x[k] = s_bx[k];
-                    s_v[k] = s_bv[k];
-                }
-            }
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i) beam_load<T>(w[i], x, i0 + i < p.NV ? at(i0 + i, tid) : p.V, p.V, mis);
         }
     };
 
-    for (int b = 0; b < batches; ++b) {
-        cp_async_wait<1>();
-        __syncthreads();   // batch b is there, and everything of batch b - 1 is done
-        if (b > 0) settle(b - 1, false);
-        fetch(b + 2);
-        if (tid == 0) s_new[(b + 1) % 3] = 0;
-
-        // ---- the thread's elements; past the row's end -inf ----
-        const int v0 = first + b * BATCH;
-        const uint8_t* st = ring + (b % STAGES) * STAGE;
-        uint32_t raw[NV][4];
+    // ---- maximum and sum of exponentials (a NaN or +inf makes the sum NaN) ----
+    uint32_t raw[GROUP][4], next[GROUP][4];
+    load(next, 0);
+    float m = NEG_INF, sum = 0.f;
+    for (int i0 = 0; i0 < p.NV; i0 += GROUP) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const uint4 lo = *reinterpret_cast<const uint4*>(st + (i * THREADS + tid) * 16);
-            raw[i][0] = lo.x; raw[i][1] = lo.y; raw[i][2] = lo.z; raw[i][3] = lo.w;
-        }
-        if (mis != 0) {
+        for (int i = 0; i < GROUP; ++i)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const uint4 hi = *reinterpret_cast<const uint4*>(st + (i * THREADS + tid) * 16 + 16);
-                uint32_t q[8] = {raw[i][0], raw[i][1], raw[i][2], raw[i][3], hi.x, hi.y, hi.z, hi.w};
-                if (mis & 8) {
-#pragma unroll
-                    for (int j = 0; j < 6; ++j) q[j] = q[j + 2];
-                }
-                if (mis & 4) {
-#pragma unroll
-                    for (int j = 0; j < 5; ++j) q[j] = q[j + 1];
-                }
-                const int bits = 8 * (mis & 3);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) raw[i][j] = __funnelshift_r(q[j], q[j + 1], bits);
-            }
-        }
-        if (v0 + BATCH > p.V) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = v0 + (i * THREADS + tid) * VEC;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) raw[i][j] = E::cut(raw[i][j], p.V - v - j * (4 / ESZ));
-            }
-        }
-
-        // ---- maximum and sum of exponentials (a NaN or +inf makes the sum NaN) ----
+            for (int j = 0; j < 4; ++j) raw[i][j] = next[i][j];
+        if (i0 + GROUP < p.NV) load(next, i0 + GROUP);
         uint32_t wm = raw[0][0];
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < GROUP; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) wm = E::word_max(wm, raw[i][j]);
         const float mine = E::top(wm);
@@ -392,43 +277,13 @@ __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamPa
         const float ref = m > NEG_INF ? m : 0.f;
         float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < GROUP; ++i)
 #pragma unroll
             for (int q = 0; q < VEC / 2; ++q) {
                 const float2 d = mul2(add2(E::pair(raw[i], q), make_float2(-ref, -ref)), make_float2(LOG2E, LOG2E));
                 part = add2(part, make_float2(fast_exp2(d.x), fast_exp2(d.y)));
             }
         sum += part.x + part.y;
-
-        // ---- elements that may belong to the K best: the warp looks through the
-        // elements of each thread whose maximum passes, one a lane ----
-        if (b == 0) thr = group_threshold(mine, p.K, s_key, &s_thr);
-        uint32_t pass = __ballot_sync(0xffffffffu, mine > NEG_INF && (b == 0 ? mine >= thr : mine > thr));
-        while (pass != 0) {
-            const int from = __ffs(pass) - 1;
-            pass &= pass - 1;
-            const int o = ((lane / VEC) * THREADS + (tid - lane + from)) * VEC + lane % VEC;
-            float e = NEG_INF;
-            if (lane < NV * VEC && v0 + o < p.V) e = E::one(st + mis + o * ESZ);
-            const bool in = e > NEG_INF && (b == 0 ? e >= thr : e > thr);
-            const uint32_t who = __ballot_sync(0xffffffffu, in);
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&s_new[b % 3], __popc(who));
-            at = held + __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-            if (in && at < BUF) {
-                s_x[at] = e;
-                s_v[at] = v0 + o;
-            }
-        }
-    }
-    __syncthreads();
-    settle(batches - 1, true);
-    {
-        const size_t at = (static_cast<size_t>(row) * p.S + blockIdx.x) * p.K;
-        for (int k = tid; k < p.K; k += THREADS) {
-            p.cand_x[at + k] = k < held ? s_bx[k] : NEG_INF;
-            p.cand_v[at + k] = k < held ? s_bv[k] : -1;
-        }
     }
 
     // ---- the segment's maximum and sum ----
@@ -436,24 +291,85 @@ __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamPa
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     if (lane == 0) s_m[tid >> 5] = top;
-    __syncthreads();
+    const float thr = from_key(kth_key(order_key(m), p.K));   // its barriers cover s_m and s_n
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, s_m[w]);
     double total = m == top ? sum : sum * fast_exp2((m - top) * LOG2E);   // equal infinities have no difference
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
     if (lane == 0) s_sum[tid >> 5] = total;
+
+    // ---- the K best: the warp reads the elements of each thread that reaches
+    // the threshold again, a vector a lane ----
+    uint32_t pass = __ballot_sync(0xffffffffu, m > NEG_INF && m >= thr);
+    while (pass != 0) {
+        const int from = tid - lane + __ffs(pass) - 1;
+        pass &= pass - 1;
+        for (int i = lane; i < p.NV; i += 32) {
+            const int v = at(i, from);
+            uint32_t w[4];
+            beam_load<T>(w, x, v, p.V, mis);
+#pragma unroll
+            for (int q = 0; q < VEC / 2; ++q) {
+                const float2 e = E::pair(w, q);
+                if (e.x >= thr && e.x > NEG_INF) {
+                    const int k = atomicAdd(&s_n, 1);
+                    if (k < BUF) s_c[k] = pack(e.x, v + 2 * q);
+                }
+                if (e.y >= thr && e.y > NEG_INF) {
+                    const int k = atomicAdd(&s_n, 1);
+                    if (k < BUF) s_c[k] = pack(e.y, v + 2 * q + 1);
+                }
+            }
+        }
+    }
     __syncthreads();
+    const size_t part = static_cast<size_t>(row) * p.S + blockIdx.x;
     if (tid == 0) {
         total = 0;
 #pragma unroll
         for (int w = 0; w < THREADS / 32; ++w) total += s_sum[w];
-        p.sums[static_cast<size_t>(row) * p.S + blockIdx.x] = make_float2(top, static_cast<float>(total));
+        p.sums[part] = make_float2(top, static_cast<float>(total));
     }
-}
-template <class T, int NV>
-constexpr int beam_smem() {
-    return bm::STAGES * (NV * bm::Elem<T>::VEC * bm::THREADS * static_cast<int>(sizeof(T)) + 16);
+    uint64_t* out = p.cand + part * p.K;
+    const int n = s_n;
+    if (n <= BUF) {
+        for (int i = tid; i < n; i += THREADS) {
+            const uint64_t c = s_c[i];
+            const int rank = beam_rank(s_c, n, c);
+            if (rank < p.K) out[rank] = c;
+        }
+        for (int k = n + tid; k < p.K; k += THREADS) out[k] = 0;
+        return;
+    }
+    // ---- more than the buffer holds: one after another ----
+    uint64_t last = ~0ull;
+    for (int k = 0; k < p.K; ++k) {
+        uint64_t best = 0;
+        for (int i = 0; i < p.NV; ++i) {
+            const int v = at(i, tid);
+            uint32_t w[4];
+            beam_load<T>(w, x, v, p.V, mis);
+#pragma unroll
+            for (int q = 0; q < VEC / 2; ++q) {
+                const float2 e = E::pair(w, q);
+                const uint64_t c0 = pack(e.x, v + 2 * q), c1 = pack(e.y, v + 2 * q + 1);
+                if (e.x > NEG_INF && c0 < last && c0 > best) best = c0;
+                if (e.y > NEG_INF && c1 < last && c1 > best) best = c1;
+            }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            const uint64_t c = __shfl_xor_sync(0xffffffffu, best, d);
+            best = c > best ? c : best;
+        }
+        __syncthreads();   // the last round's readers are done
+        if (lane == 0) s_c[tid >> 5] = best;
+        __syncthreads();
+        for (int w = 0; w < THREADS / 32; ++w) best = s_c[w] > best ? s_c[w] : best;
+        if (tid == 0) out[k] = best;   // more than K elements are above -inf
+        last = best;
+    }
 }
 
 // One block per request.
@@ -461,8 +377,6 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
     using namespace bm;
     __shared__ double s_lse[MAX_K], s_cum[MAX_K];   // per beam; a beam without candidates has lse NaN
     __shared__ uint8_t s_done[MAX_K];
-    __shared__ uint32_t s_key[128];
-    __shared__ float s_thr;
     __shared__ double s_score[MERGE_BUF];
     __shared__ int s_flat[MERGE_BUF], s_n;
     const int tid = threadIdx.x, lane = tid & 31, g = blockIdx.x;
@@ -513,10 +427,10 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
             }
         } else if (state == 0) {
             const size_t at = static_cast<size_t>(g * p.W + w) * SK + q;
-            const float x = p.cand_x[at];
-            if (x > NEG_INF) {
-                key = s_cum[w] + (x - s_lse[w]);
-                *flat += p.cand_v[at];
+            const uint64_t c = p.cand[at];
+            if (c != 0) {
+                key = s_cum[w] + (value_of(c) - s_lse[w]);
+                *flat += static_cast<int>(index_of(c));
             }
         }
         return key > NEG_INF ? key : static_cast<double>(NEG_INF);   // a NaN has no place
@@ -528,7 +442,7 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
     }
     // scores rounded to 32 bits keep their order up to ties, so the threshold
     // on them lets every candidate of the K best through
-    const float thr = group_threshold(mine, p.K, s_key, &s_thr);
+    const float thr = from_key(kth_key(order_key(mine), p.K));
     if (mine >= thr)
         for (int c = tid; c < C; c += THREADS) {
             int flat;
@@ -557,8 +471,11 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
             const double key = s_score[i];
             const int flat = s_flat[i];
             int rank = 0;
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) rank += s_score[j] > key || (s_score[j] == key && s_flat[j] < flat);
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) {
+                const double other = s_score[j];
+                rank += (other > key) | ((other == key) & (s_flat[j] < flat));
+            }
             if (rank < p.K) put(rank, key, flat);
         }
         for (int k = n + tid; k < p.K; k += THREADS) put(k, NEG_INF, 0);

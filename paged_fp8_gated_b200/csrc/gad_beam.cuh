@@ -140,10 +140,11 @@ __device__ __forceinline__ uint64_t pack(float x, uint32_t v) {
 __device__ __forceinline__ float value_of(uint64_t c) { return from_key(static_cast<uint32_t>(c >> 32)); }
 __device__ __forceinline__ uint32_t index_of(uint64_t c) { return 0xffffffffu - static_cast<uint32_t>(c); }
 
-// A value that at least K of the threads' keys reach, the largest there is or
-// one that exactly K reach: bisection over the key's bits, a counting barrier a
-// bit (about 16 of them; taking maxima out one by one costs 200 cycles each).
-// All threads call it; its first barrier also covers what they wrote before.
+// A value that at least K of the threads' keys reach, and as far as their bits
+// tell them apart no more than K + K / 4 + 2: bisection over the key's bits, a
+// counting barrier a bit (about 12 of them; taking maxima out one by one costs
+// 200 cycles each).  All threads call it; its first barrier also covers what
+// they wrote before.
 __device__ __forceinline__ uint32_t kth_key(uint32_t key, int K) {
     uint32_t t = 0;
     for (int bit = 31; bit >= 0; --bit) {
@@ -151,7 +152,7 @@ __device__ __forceinline__ uint32_t kth_key(uint32_t key, int K) {
         const int c = __syncthreads_count(key >= up);
         if (c >= K) {
             t = up;
-            if (c == K) break;
+            if (c <= K + K / 4 + 2) break;
         }
     }
     return t;
@@ -303,24 +304,30 @@ __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamPa
     // the threshold again, a vector a lane ----
     uint32_t pass = __ballot_sync(0xffffffffu, m > NEG_INF && m >= thr);
     while (pass != 0) {
+        // two threads' vectors at a time
         const int from = tid - lane + __ffs(pass) - 1;
         pass &= pass - 1;
+        const int other = pass != 0 ? tid - lane + __ffs(pass) - 1 : -1;
+        pass &= pass - 1;
         for (int i = lane; i < p.NV; i += 32) {
-            const int v = at(i, from);
-            uint32_t w[4];
-            beam_load<T>(w, x, v, p.V, mis);
+            const int v[2] = {at(i, from), other >= 0 ? at(i, other) : p.V};
+            uint32_t w[2][4];
+            beam_load<T>(w[0], x, v[0], p.V, mis);
+            beam_load<T>(w[1], x, v[1], p.V, mis);
 #pragma unroll
-            for (int q = 0; q < VEC / 2; ++q) {
-                const float2 e = E::pair(w, q);
-                if (e.x >= thr && e.x > NEG_INF) {
-                    const int k = atomicAdd(&s_n, 1);
-                    if (k < BUF) s_c[k] = pack(e.x, v + 2 * q);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < VEC / 2; ++q) {
+                    const float2 e = E::pair(w[h], q);
+                    if (e.x >= thr && e.x > NEG_INF) {
+                        const int k = atomicAdd(&s_n, 1);
+                        if (k < BUF) s_c[k] = pack(e.x, v[h] + 2 * q);
+                    }
+                    if (e.y >= thr && e.y > NEG_INF) {
+                        const int k = atomicAdd(&s_n, 1);
+                        if (k < BUF) s_c[k] = pack(e.y, v[h] + 2 * q + 1);
+                    }
                 }
-                if (e.y >= thr && e.y > NEG_INF) {
-                    const int k = atomicAdd(&s_n, 1);
-                    if (k < BUF) s_c[k] = pack(e.y, v + 2 * q + 1);
-                }
-            }
         }
     }
     __syncthreads();
@@ -381,21 +388,32 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
     __shared__ int s_flat[MERGE_BUF], s_n;
     const int tid = threadIdx.x, lane = tid & 31, g = blockIdx.x;
     pdl_wait_primary();
+    const int SK = p.S * p.K;
+    const int C = p.W * SK;   // candidate c of the request: list (w, s), place k
+    // the thread's first candidates, on their way while the sums are joined
+    constexpr int EARLY = 4;
+    uint64_t early[EARLY];
+#pragma unroll
+    for (int e = 0; e < EARLY; ++e) {
+        const int c = tid + e * THREADS;
+        early[e] = c < C ? p.cand[static_cast<size_t>(g) * C + c] : 0;
+    }
     if (tid == 0) s_n = 0;
     for (int w = tid >> 5; w < p.W; w += THREADS / 32) {
         const int row = g * p.W + w;
+        const float2* ms = p.sums + static_cast<size_t>(row) * p.S;
+        const float2 mine = lane < p.S ? ms[lane] : make_float2(NEG_INF, 0.f);   // not written for some rows
         const float cum = p.scores[row];
         const bool done = p.finished != nullptr && p.finished[row] != 0;
         double lse = 0;
         if (!done && cum > NEG_INF) {
-            const float2* ms = p.sums + static_cast<size_t>(row) * p.S;
-            float m = NEG_INF;
-            for (int s = lane; s < p.S; s += 32) m = fmaxf(m, ms[s].x);
+            float m = fmaxf(mine.x, NEG_INF);
+            for (int s = lane + 32; s < p.S; s += 32) m = fmaxf(m, ms[s].x);
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
             double sum = 0;
             for (int s = lane; s < p.S; s += 32) {
-                const float2 q = ms[s];
+                const float2 q = s == lane ? mine : ms[s];
                 // a segment without a finite logit adds nothing, unless it holds a NaN
                 sum += q.x > NEG_INF ? q.y * exp(static_cast<double>(q.x) - m)
                                      : static_cast<double>(q.y != q.y ? q.y : 0.f);
@@ -412,10 +430,7 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
     }
     __syncthreads();
 
-    // candidate c of the request: list (w, s), place k
-    const int SK = p.S * p.K;
-    const int C = p.W * SK;
-    auto score = [&](int c, int* flat) -> double {
+    auto score = [&](int c, uint64_t cand, int* flat) -> double {
         const int w = c / SK, q = c - w * SK;
         const int state = s_done[w];
         double key = NEG_INF;
@@ -425,28 +440,36 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
                 key = s_cum[w];
                 *flat += p.pad;
             }
-        } else if (state == 0) {
-            const size_t at = static_cast<size_t>(g * p.W + w) * SK + q;
-            const uint64_t c = p.cand[at];
-            if (c != 0) {
-                key = s_cum[w] + (value_of(c) - s_lse[w]);
-                *flat += static_cast<int>(index_of(c));
-            }
+        } else if (state == 0 && cand != 0) {
+            key = s_cum[w] + (value_of(cand) - s_lse[w]);
+            *flat += static_cast<int>(index_of(cand));
         }
         return key > NEG_INF ? key : static_cast<double>(NEG_INF);   // a NaN has no place
     };
+    // f(key, flat) over the thread's candidates
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int e = 0; e < EARLY; ++e) {
+            const int c = tid + e * THREADS;
+            if (c < C) {
+                int flat;
+                const double key = score(c, early[e], &flat);
+                f(key, flat);
+            }
+        }
+        for (int c = tid + EARLY * THREADS; c < C; c += THREADS) {
+            int flat;
+            const double key = score(c, p.cand[static_cast<size_t>(g) * C + c], &flat);
+            f(key, flat);
+        }
+    };
     float mine = NEG_INF;
-    for (int c = tid; c < C; c += THREADS) {
-        int flat;
-        mine = fmaxf(mine, static_cast<float>(score(c, &flat)));
-    }
+    each([&](double key, int) { mine = fmaxf(mine, static_cast<float>(key)); });
     // scores rounded to 32 bits keep their order up to ties, so the threshold
     // on them lets every candidate of the K best through
     const float thr = from_key(kth_key(order_key(mine), p.K));
     if (mine >= thr)
-        for (int c = tid; c < C; c += THREADS) {
-            int flat;
-            const double key = score(c, &flat);
+        each([&](double key, int flat) {
             if (static_cast<float>(key) >= thr && key > NEG_INF) {
                 const int k = atomicAdd(&s_n, 1);
                 if (k < MERGE_BUF) {
@@ -454,7 +477,7 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
                     s_flat[k] = flat;
                 }
             }
-        }
+        });
     __syncthreads();
     const int n = s_n;
     float* out_s = p.out_scores + static_cast<size_t>(g) * p.K;
@@ -485,15 +508,13 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
         for (int k = 0; k < p.K; ++k) {
             double bk = NEG_INF;
             int bf = 0x7fffffff;
-            for (int c = tid; c < C; c += THREADS) {
-                int flat;
-                const double key = score(c, &flat);
+            each([&](double key, int flat) {
                 const bool behind = key < last || (key == last && flat > last_f);
                 if (behind && key > NEG_INF && (key > bk || (key == bk && flat < bf))) {
                     bk = key;
                     bf = flat;
                 }
-            }
+            });
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) {
                 const double ok = __shfl_xor_sync(0xffffffffu, bk, d);

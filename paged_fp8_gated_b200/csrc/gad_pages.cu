@@ -19,11 +19,11 @@ PagesWs pages_ws(long long num_pages) {
     w.head_off = off;
     off = align_up(off + sizeof(gad::pg::Head));
     w.counts_off = off;
-    off = align_up(off + gad::pg::MAX_CHUNKS * sizeof(int));
+    off = align_up(off + gad::pg::MAX_CHUNKS * sizeof(unsigned));
     w.rows_off = off;
     off = align_up(off + 2 * gad::pg::MAX_ROWS * sizeof(int));
     w.prefix_off = off;
-    off = align_up(off + (gad::pg::MAX_ROWS + 1) * sizeof(long long));
+    off = align_up(off + (gad::pg::MAX_ROWS + 1) * sizeof(int));
     w.rank_off = off;
     off = align_up(off + static_cast<size_t>(num_pages) * sizeof(int));
     w.total = off;
@@ -36,9 +36,9 @@ gad::pg::Ws bind_ws(void* workspace, long long num_pages) {
     uint8_t* b = static_cast<uint8_t*>(workspace);
     gad::pg::Ws ws;
     ws.head = reinterpret_cast<gad::pg::Head*>(b + w.head_off);
-    ws.counts = reinterpret_cast<int*>(b + w.counts_off);
+    ws.counts = reinterpret_cast<unsigned*>(b + w.counts_off);
     ws.rows = reinterpret_cast<int*>(b + w.rows_off);
-    ws.prefix = reinterpret_cast<long long*>(b + w.prefix_off);
+    ws.prefix = reinterpret_cast<int*>(b + w.prefix_off);
     ws.rank = reinterpret_cast<int*>(b + w.rank_off);
     return ws;
 }
@@ -86,11 +86,11 @@ int check_device() {
 }
 
 template <class... Params, class... Args>
-int launch(const char* name, void (*kern)(Params...), dim3 grid, cudaStream_t s, bool pdl, Args... args) {
+int launch(const char* name, void (*kern)(Params...), dim3 grid, int threads, cudaStream_t s, bool pdl, Args... args) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(gad::pg::THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.stream = s;
     cudaLaunchAttribute attr = pdl_attr();
     cfg.attrs = &attr;
@@ -99,6 +99,8 @@ int launch(const char* name, void (*kern)(Params...), dim3 grid, cudaStream_t s,
     if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(e));
     return GAD_OK;
 }
+
+constexpr int kThreads = gad::pg::THREADS;
 
 int shift_of(int page_size) { return page_size == 64 ? 6 : 0; }
 
@@ -153,8 +155,9 @@ int gad_pages_copy(void* const* caches, int n_caches, size_t page_bytes, int64_t
     for (int c0 = 0; c0 < n_caches; c0 += gad::pg::MAX_CACHES) {
         const int m = n_caches - c0 < gad::pg::MAX_CACHES ? n_caches - c0 : gad::pg::MAX_CACHES;
         for (int i = 0; i < m; ++i) p.cache[i] = static_cast<uint8_t*>(caches[c0 + i]);
-        const dim3 grid(gx, static_cast<unsigned>(m));
-        st = launch("page copy", wide ? gad::pages_copy_kernel<true> : gad::pages_copy_kernel<false>, grid,
+        p.caches = m;
+        const dim3 grid(gx, static_cast<unsigned>(wide ? m : (m + 1) / 2));
+        st = launch("page copy", wide ? gad::pages_copy_kernel<true> : gad::pages_copy_kernel<false>, grid, kThreads,
                     static_cast<cudaStream_t>(stream), false, p);
         if (st != GAD_OK) return st;
     }
@@ -201,12 +204,12 @@ int gad_pages_fork(const int32_t* page_table, const int32_t* lens, int rows_in, 
     p.ws = bind_ws(workspace, num_pages);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = max_pages % 4 == 0 && aligned(page_table, 16) && aligned(out_table, 16);
-    const dim3 grid(blocks(max_pages, gad::pg::COLS), static_cast<unsigned>(rows_in > rows_out ? rows_in : rows_out));
-    st = launch("fork", vec ? gad::fork_kernel<true> : gad::fork_kernel<false>, grid, s, false, p);
+    const dim3 grid(blocks(max_pages, gad::pg::COLS), blocks(rows_in > rows_out ? rows_in : rows_out, gad::pg::ROWS));
+    st = launch("fork", vec ? gad::fork_kernel<true> : gad::fork_kernel<false>, grid, kThreads, s, false, p);
     if (st != GAD_OK || page_size == 1) return st;   // single-token pages are never partly filled
-    st = launch("fork count", gad::fork_count_kernel, dim3(p.pool.chunks + 1), s, true, p);
+    st = launch("fork count", gad::fork_count_kernel, dim3(p.pool.chunks + 1), kThreads, s, true, p);
     if (st != GAD_OK) return st;
-    return launch("fork assign", gad::fork_assign_kernel, dim3(p.pool.chunks), s, true, p,
+    return launch("fork assign", gad::fork_assign_kernel, dim3(p.pool.chunks), kThreads, s, true, p,
                   static_cast<int>(GAD_STATUS_PAGES_POOL));
 }
 
@@ -239,13 +242,13 @@ int gad_pages_extend(int32_t* page_table, int32_t* lens, int rows, int L, int ma
     p.pool = bind_pool(refs, num_pages);
     p.ws = bind_ws(workspace, num_pages);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = launch("extend count", gad::extend_count_kernel, dim3(p.pool.chunks + 1), s, false, p);
+    st = launch("extend count", gad::extend_count_kernel, dim3(p.pool.chunks + 1), kThreads, s, false, p);
     if (st != GAD_OK) return st;
     // enough blocks for the tokens' rows too
     const long long tok = (static_cast<long long>(rows) * L + 8 * gad::pg::THREADS - 1) / (8 * gad::pg::THREADS);
     const long long grid = tok > 1024 ? 1024 : tok;
     return launch("extend assign", gad::extend_assign_kernel,
-                  dim3(static_cast<unsigned>(grid > p.pool.chunks ? grid : p.pool.chunks)), s, true, p,
+                  dim3(static_cast<unsigned>(grid > p.pool.chunks ? grid : p.pool.chunks)), kThreads, s, true, p,
                   static_cast<int>(GAD_STATUS_PAGES_POOL), static_cast<int>(GAD_STATUS_PAGES_ROW));
 }
 
@@ -270,7 +273,7 @@ int gad_pages_free(const int32_t* page_table, int32_t* lens, int rows, const uin
     p.refs = refs;
     p.num_pages = num_pages;
     return launch("free", gad::free_kernel, dim3(static_cast<unsigned>(rows) * gad::pg::FREE_CLUSTER),
-                  static_cast<cudaStream_t>(stream), false, p);
+                  gad::pg::FREE_THREADS, static_cast<cudaStream_t>(stream), false, p);
 }
 
 int gad_pages_compact(int32_t* page_table, const int32_t* lens, int rows, int max_pages, int page_size, int32_t* refs,
@@ -303,13 +306,13 @@ int gad_pages_compact(int32_t* page_table, const int32_t* lens, int rows, int ma
     p.pool = bind_pool(refs, num_pages);
     p.ws = bind_ws(workspace, num_pages);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = launch("compact count", gad::compact_count_kernel, dim3(p.pool.chunks), s, false, p);
+    st = launch("compact count", gad::compact_count_kernel, dim3(p.pool.chunks), kThreads, s, false, p);
     if (st != GAD_OK) return st;
-    st = launch("compact rank", gad::compact_rank_kernel, dim3(p.pool.chunks), s, true, p);
+    st = launch("compact rank", gad::compact_rank_kernel, dim3(p.pool.chunks), kThreads, s, true, p);
     if (st != GAD_OK) return st;
-    const unsigned gx = blocks(max_pages, 8 * gad::pg::THREADS);
+    const unsigned gx = blocks(max_pages, 4 * gad::pg::THREADS);
     return launch("compact apply", gad::compact_apply_kernel,
-                  dim3(gx < 1024 ? gx : 1024, static_cast<unsigned>(rows) + 1), s, true, p);
+                  dim3(gx < 1024 ? gx : 1024, static_cast<unsigned>(rows) + 1), kThreads, s, true, p);
 }
 
 }  // extern "C"

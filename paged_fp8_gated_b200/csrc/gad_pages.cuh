@@ -11,10 +11,10 @@
 // them changes nothing.
 //
 // Handing out pages needs the k-th free page for k = 0, 1, ...: one pass counts
-// the free pages per chunk of the pool (count_kernel), a second one ranks the
-// free pages of each chunk behind the sum of the chunks before it and gives
-// each to its row.  Both read the counts once (4 bytes a page).  Page ids
-// outside [0, num_pages) are skipped everywhere.
+// the free pages per chunk of the pool, a second one ranks the free pages of
+// each chunk behind the sum of the chunks before it and gives each to its row.
+// Both read the counts once (4 bytes a page).  Page ids outside [0, num_pages)
+// are skipped everywhere.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -29,8 +29,11 @@ constexpr int THREADS = 256;
 constexpr int CHUNK = 4096;          // pages per chunk, unless the pool has more than MAX_CHUNKS of them
 constexpr int MAX_CHUNKS = 1024;
 constexpr int MAX_ROWS = 4096;
-constexpr int COLS = 4096;           // table columns per block
+constexpr int COLS = 4 * THREADS;    // fork: table columns per block, four a thread
+constexpr int ROWS = 8;              // fork: table rows per block
+constexpr int RUN = CHUNK / THREADS; // pages of a chunk that a thread looks at
 constexpr int FREE_CLUSTER = 8;      // blocks that share a row in free_kernel
+constexpr int FREE_THREADS = 1024;
 constexpr int MAX_CACHES = 64;       // caches per copy launch
 
 // Pages per chunk: CHUNK, or the smallest multiple of it with at most MAX_CHUNKS chunks.
@@ -46,15 +49,15 @@ struct Head {
     int need_list;        // fork: rows that need a fresh page
     int row_overflow;     // extend: a row would outgrow the table
     int moves;            // compact: pages that move
-    long long need;       // extend: pages that are needed in all
-    long long total;      // compact: pages in use
+    int need;             // extend: pages that are needed in all (at most 2^28)
+    int total;            // compact: pages in use
 };
 
 struct Ws {
     Head* head;
-    int* counts;          // [MAX_CHUNKS] free pages per chunk
+    unsigned* counts;     // [MAX_CHUNKS] free pages per chunk
     int* rows;            // [2 MAX_ROWS] per-row values
-    long long* prefix;    // [MAX_ROWS + 1]
+    int* prefix;          // [MAX_ROWS + 1]
     int* rank;            // [num_pages], compact
 };
 
@@ -98,16 +101,20 @@ __device__ __forceinline__ int block_scan(int v, int* total) {
     *total = all;
     return before + x - v;
 }
-__device__ __forceinline__ long long block_sum(long long v) {
-    __shared__ long long warp_sum[THREADS / 32];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+// Sums of a and b over the block's threads (below 2^32).
+__device__ __forceinline__ uint2 block_sum2(unsigned a, unsigned b) {
+    __shared__ uint2 warp_sum[THREADS / 32];
+    a = __reduce_add_sync(0xffffffffu, a);
+    b = __reduce_add_sync(0xffffffffu, b);
+    __syncthreads();  // the previous call's readers are done
+    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = make_uint2(a, b);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = v;
-    __syncthreads();
-    long long s = 0;
+    uint2 s = make_uint2(0, 0);
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) s += warp_sum[w];
+    for (int w = 0; w < THREADS / 32; ++w) {
+        s.x += warp_sum[w].x;
+        s.y += warp_sum[w].y;
+    }
     return s;
 }
 
@@ -122,17 +129,52 @@ __device__ __forceinline__ int4 refs4(const Pool& p, long long i, int past) {
     return r;
 }
 
-// Free pages in the chunks before `chunk`, and in all of them.
-__device__ __forceinline__ void free_before(const Ws& ws, int chunks, int chunk, long long* before,
-                                            long long* total) {
-    long long b = 0, t = 0;
+// Which of the RUN pages from i on are free, as bits (i a multiple of 4).
+__device__ __forceinline__ unsigned free_bits(const Pool& p, long long i, long long end) {
+    unsigned bits = 0;
+#pragma unroll
+    for (int u = 0; u < RUN / 4; ++u) {
+        const long long at = i + 4 * u;
+        const int4 r = at < end ? refs4(p, at, 1) : make_int4(1, 1, 1, 1);
+        bits |= static_cast<unsigned>((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << 4 * u;
+    }
+    return bits;
+}
+__device__ __forceinline__ long long chunk_end(const Pool& p, int chunk) {
+    const long long e = (chunk + 1) * p.chunk;
+    return e < p.num_pages ? e : p.num_pages;
+}
+// Free pages of a chunk (all threads get the sum).
+__device__ __forceinline__ unsigned count_chunk(const Pool& p, int chunk) {
+    const long long end = chunk_end(p, chunk);
+    unsigned n = 0;
+    for (long long i = chunk * p.chunk + RUN * threadIdx.x; i < end; i += CHUNK) n += __popc(free_bits(p, i, end));
+    return block_sum2(n, 0).x;
+}
+// Free pages in the chunks before `chunk` (x), and in all of them (y).
+__device__ __forceinline__ uint2 free_before(const Ws& ws, int chunks, int chunk) {
+    unsigned b = 0, t = 0;
     for (int i = threadIdx.x; i < chunks; i += THREADS) {
-        const int c = ws.counts[i];
+        const unsigned c = ws.counts[i];
         t += c;
         if (i < chunk) b += c;
     }
-    *before = block_sum(b);
-    *total = block_sum(t);
+    return block_sum2(b, t);
+}
+// give(page, k) for the free pages of a chunk whose rank k is below `need`;
+// `before`: free pages before the chunk; `bits`: free_bits of its first CHUNK pages.
+template <class F>
+__device__ __forceinline__ void hand_out(const Pool& p, int chunk, unsigned bits, long long before, long long need,
+                                         F give) {
+    const long long end = chunk_end(p, chunk);
+    for (long long i0 = chunk * p.chunk; i0 < end && before < need; i0 += CHUNK) {
+        const long long mine = i0 + RUN * threadIdx.x;
+        if (i0 != chunk * p.chunk) bits = mine < end ? free_bits(p, mine, end) : 0;
+        int sum;
+        long long k = before + block_scan(__popc(bits), &sum);
+        for (; bits != 0 && k < need; ++k, bits &= bits - 1) give(mine + __ffs(bits) - 1, k);
+        before += sum;
+    }
 }
 
 }  // namespace pg
@@ -149,74 +191,106 @@ struct ForkParams {
     pg::Ws ws;
 };
 
-// One block per (COLS columns, row): the row's old pages change their counts
-// by its children - 1 (of a partly filled last page only the first child takes
-// the page, so its count only falls when there is none), and the new row of
-// that number takes its parent's entries.  The entry of a fresh last page is
-// left to fork_assign_kernel.
+// One block per (COLS columns, ROWS rows).  An old row's pages change their
+// counts by its children - 1 (of a partly filled last page only the first child
+// takes the page, so its count only falls when there is none); a new row takes
+// its parent's entries.  The entry of a fresh last page is left to
+// fork_assign_kernel.  Rows that share pages are usually neighbours (the beams
+// of a request): a thread adds up what its rows change about the page that they
+// have in common in a column, and a count is touched only if something is left.
 template <bool VEC>
 __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
     using namespace pg;
-    __shared__ int s_kids, s_elder;
-    const int y = blockIdx.y, tid = threadIdx.x;
+    __shared__ int s_kids[ROWS], s_elder[ROWS], s_par[ROWS], s_len[ROWS], s_new[ROWS];
+    const int y0 = blockIdx.y * ROWS, tid = threadIdx.x;
     pdl_launch_dependents();
-    if (tid == 0) s_kids = s_elder = 0;
+    if (tid < ROWS) {
+        const int y = y0 + tid;
+        int par = y < p.rows_out ? p.parent[y] : -1;
+        if (par >= p.rows_in) par = -1;
+        s_kids[tid] = s_elder[tid] = 0;
+        s_par[tid] = par;
+        s_len[tid] = y < p.rows_in ? p.lens[y] : -1;
+        s_new[tid] = par >= 0 ? p.lens[par] : -1;
+    }
     __syncthreads();
-    const int par = y < p.rows_out ? p.parent[y] : -1;
-    const bool alive = par >= 0 && par < p.rows_in;
-    int kids = 0, elder = 0;
     for (int r = tid; r < p.rows_out; r += THREADS) {
         const int q = p.parent[r];
-        kids += q == y;
-        elder |= r < y && q == par;
+        if (q >= y0 && q < y0 + ROWS) atomicAdd(&s_kids[q - y0], 1);
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k)
+            if (r < y0 + k && q == s_par[k]) s_elder[k] = 1;
     }
-    if (kids) atomicAdd(&s_kids, kids);
-    if (elder) s_elder = 1;
     __syncthreads();
-    kids = s_kids;
-    const bool fresh_last = alive && s_elder;   // and the parent's last page is partly filled (below)
 
     const int c0 = blockIdx.x * COLS;
-    if (y < p.rows_in && kids != 1) {
-        const int len = p.lens[y];
+    auto col = [&](int u) { return VEC ? c0 + 4 * tid + u : c0 + u * THREADS + tid; };
+    // the four entries of a row (any value from `n` on)
+    auto entries = [&](int (&e)[4], const int* row, int n) {
+        if (VEC) {
+            const int4 q = col(0) < n ? *reinterpret_cast<const int4*>(row + col(0)) : make_int4(-1, -1, -1, -1);
+            e[0] = q.x; e[1] = q.y; e[2] = q.z; e[3] = q.w;
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) e[u] = col(u) < n ? row[col(u)] : -1;
+        }
+    };
+    int page[4] = {-1, -1, -1, -1}, left[4] = {0, 0, 0, 0};
+    auto flush = [&](int u) {
+        if (left[u] != 0 && page[u] >= 0 && page[u] < p.pool.num_pages) atomicAdd(p.pool.refs + page[u], left[u]);
+    };
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        const int kids = s_kids[k], len = s_len[k];
         const int n = pages_of(len, p.shift, p.max_pages);
+        if (kids == 1 || n <= c0) continue;
         const int last = has_partial(len, p.shift, p.max_pages) ? n - 1 : -1;
-        const int* row = p.table + static_cast<size_t>(y) * p.max_pages;
-        const int end = min(n, c0 + COLS);
-        for (int j = c0 + tid; j < end; j += THREADS) {
-            const int page = row[j];
-            const int d = (j == last ? min(kids, 1) : kids) - 1;
-            if (d != 0 && page >= 0 && page < p.pool.num_pages) atomicAdd(p.pool.refs + page, d);
+        int e[4];
+        entries(e, p.table + static_cast<size_t>(y0 + k) * p.max_pages, n);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (col(u) >= n) continue;
+            const int d = (col(u) == last ? min(kids, 1) : kids) - 1;
+            if (e[u] != page[u]) {
+                flush(u);
+                page[u] = e[u];
+                left[u] = 0;
+            }
+            left[u] += d;
         }
     }
-    if (y < p.rows_out) {
-        const int len = alive ? p.lens[par] : -1;
-        int n = pages_of(len, p.shift, p.max_pages);
-        const bool fresh = fresh_last && has_partial(len, p.shift, p.max_pages);
-        if (fresh) --n;
-        const int* src = p.table + static_cast<size_t>(alive ? par : 0) * p.max_pages;
-        int* dst = p.out_table + static_cast<size_t>(y) * p.max_pages;
-        const int end = min(n, c0 + COLS);
-        if (VEC) {
-            const int end4 = c0 + (end > c0 ? (end - c0) / 4 * 4 : 0);
-            for (int j = c0 + 4 * tid; j < end4; j += 4 * THREADS)
-                *reinterpret_cast<int4*>(dst + j) = *reinterpret_cast<const int4*>(src + j);
-            if (end4 + tid < end) dst[end4 + tid] = src[end4 + tid];
-        } else {
-            for (int j = c0 + tid; j < end; j += THREADS) dst[j] = src[j];
-        }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) flush(u);
+
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        const int y = y0 + k, len = s_new[k];
+        if (y >= p.rows_out) break;
+        const bool fresh = s_elder[k] && has_partial(len, p.shift, p.max_pages);
+        const int n = pages_of(len, p.shift, p.max_pages) - fresh;
         if (blockIdx.x == 0 && tid == 0) {
             p.out_lens[y] = len < 0 ? -1 : len;
             p.copy_src[y] = -1;
             p.copy_dst[y] = -1;
-            p.ws.rows[y] = fresh ? 1 : 0;
+            p.ws.rows[y] = fresh;
             if (y == 0) p.ws.head->status = 0;
+        }
+        if (n <= c0) continue;
+        int e[4];
+        entries(e, p.table + static_cast<size_t>(s_par[k]) * p.max_pages, n);
+        int* dst = p.out_table + static_cast<size_t>(y) * p.max_pages;
+        if (VEC && col(3) < n) {
+            *reinterpret_cast<int4*>(dst + col(0)) = make_int4(e[0], e[1], e[2], e[3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (col(u) < n) dst[col(u)] = e[u];
         }
     }
 }
 
 // Block c < chunks: free pages of chunk c.  Block `chunks`: the rows that need
-// a fresh page, in order (fork).
+// a fresh page, in order.
 __global__ void __launch_bounds__(pg::THREADS) fork_count_kernel(const ForkParams p) {
     using namespace pg;
     pdl_launch_dependents();
@@ -236,59 +310,35 @@ __global__ void __launch_bounds__(pg::THREADS) fork_count_kernel(const ForkParam
         if (tid == 0) p.ws.head->need_list = at;
         return;
     }
-    const long long i0 = blockIdx.x * p.pool.chunk;
-    const long long i1 = i0 + p.pool.chunk < p.pool.num_pages ? i0 + p.pool.chunk : p.pool.num_pages;
-    long long n = 0;
-    for (long long i = i0 + 4 * tid; i < i1; i += 4 * THREADS) {
-        const int4 r = refs4(p.pool, i, 1);
-        n += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
-    }
-    n = block_sum(n);
-    if (tid == 0) p.ws.counts[blockIdx.x] = static_cast<int>(n);
+    const unsigned n = count_chunk(p.pool, blockIdx.x);
+    if (tid == 0) p.ws.counts[blockIdx.x] = n;
 }
 
 __global__ void __launch_bounds__(pg::THREADS) fork_assign_kernel(const ForkParams p, const int pool_bit) {
     using namespace pg;
     pdl_wait_primary();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, chunk = blockIdx.x;
     const int need = p.ws.head->need_list;
     if (need == 0) return;
+    const unsigned bits = free_bits(p.pool, chunk * p.pool.chunk + RUN * tid, chunk_end(p.pool, chunk));
     const int* list = p.ws.rows + MAX_ROWS;
-    long long before, total;
-    free_before(p.ws, p.pool.chunks, blockIdx.x, &before, &total);
-    if (blockIdx.x == 0 && total < need) {
+    const uint2 f = free_before(p.ws, p.pool.chunks, chunk);
+    if (chunk == 0 && f.y < static_cast<unsigned>(need)) {
         // the pool is used up: the rows at the end of the list keep their full pages
-        for (int k = static_cast<int>(total) + tid; k < need; k += THREADS) {
+        for (int k = static_cast<int>(f.y) + tid; k < need; k += THREADS) {
             const int r = list[k];
-            const int len = p.lens[p.parent[r]];
-            p.out_lens[r] = len & ~((1 << p.shift) - 1);
+            p.out_lens[r] = p.lens[p.parent[r]] & ~((1 << p.shift) - 1);
         }
         if (tid == 0) atomicOr(&p.ws.head->status, pool_bit);
     }
-    const long long i0 = blockIdx.x * p.pool.chunk;
-    const long long i1 = i0 + p.pool.chunk < p.pool.num_pages ? i0 + p.pool.chunk : p.pool.num_pages;
-    for (long long i = i0; i < i1 && before < need; i += 4 * THREADS) {
-        const long long mine = i + 4 * tid;
-        const int4 v = mine < i1 ? refs4(p.pool, mine, 1) : make_int4(1, 1, 1, 1);
-        const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
-        int sum;
-        long long k = before + block_scan(f[0] + f[1] + f[2] + f[3], &sum);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (!f[u]) continue;
-            if (k < need) {
-                const int r = list[k], par = p.parent[r], len = p.lens[par];
-                const int page = static_cast<int>(mine + u);
-                const int j = pages_of(len, p.shift, p.max_pages) - 1;
-                p.out_table[static_cast<size_t>(r) * p.max_pages + j] = page;
-                p.copy_src[r] = p.table[static_cast<size_t>(par) * p.max_pages + j];
-                p.copy_dst[r] = page;
-                p.pool.refs[page] = 1;
-            }
-            ++k;
-        }
-        before += sum;
-    }
+    hand_out(p.pool, chunk, bits, f.x, need, [&](long long id, long long k) {
+        const int r = list[k], par = p.parent[r], page = static_cast<int>(id);
+        const int j = pages_of(p.lens[par], p.shift, p.max_pages) - 1;
+        p.out_table[static_cast<size_t>(r) * p.max_pages + j] = page;
+        p.copy_src[r] = p.table[static_cast<size_t>(par) * p.max_pages + j];
+        p.copy_dst[r] = page;
+        p.pool.refs[page] = 1;
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -310,7 +360,7 @@ __global__ void __launch_bounds__(pg::THREADS) extend_count_kernel(const ExtendP
     pdl_launch_dependents();
     const int tid = threadIdx.x;
     if (static_cast<int>(blockIdx.x) == p.pool.chunks) {
-        long long at = 0;
+        int at = 0;
         bool over = false;
         for (int r0 = 0; r0 < p.rows; r0 += THREADS) {
             const int r = r0 + tid;
@@ -327,7 +377,7 @@ __global__ void __launch_bounds__(pg::THREADS) extend_count_kernel(const ExtendP
                 }
             }
             int total;
-            const int k = block_scan(need, &total);   // at most THREADS * 65,536
+            const int k = block_scan(need, &total);
             if (r < p.rows) p.ws.prefix[r] = at + k;
             at += total;
         }
@@ -339,36 +389,31 @@ __global__ void __launch_bounds__(pg::THREADS) extend_count_kernel(const ExtendP
         }
         return;
     }
-    const long long i0 = blockIdx.x * p.pool.chunk;
-    const long long i1 = i0 + p.pool.chunk < p.pool.num_pages ? i0 + p.pool.chunk : p.pool.num_pages;
-    long long n = 0;
-    for (long long i = i0 + 4 * tid; i < i1; i += 4 * THREADS) {
-        const int4 r = refs4(p.pool, i, 1);
-        n += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
-    }
-    n = block_sum(n);
-    if (tid == 0) p.ws.counts[blockIdx.x] = static_cast<int>(n);
+    const unsigned n = count_chunk(p.pool, blockIdx.x);
+    if (tid == 0) p.ws.counts[blockIdx.x] = n;
 }
 
 __global__ void __launch_bounds__(pg::THREADS)
     extend_assign_kernel(const ExtendParams p, const int pool_bit, const int row_bit) {
     using namespace pg;
+    __shared__ int s_prefix[MAX_ROWS], s_len[MAX_ROWS];
+    const int tid = threadIdx.x, chunk = blockIdx.x;
+    const bool pool_block = chunk < p.pool.chunks;
+    // the counts change in this kernel only, a chunk by its own block
+    const unsigned bits =
+        pool_block ? free_bits(p.pool, chunk * p.pool.chunk + RUN * tid, chunk_end(p.pool, chunk)) : 0;
     pdl_wait_primary();
-    const int tid = threadIdx.x;
-    const long long need = p.ws.head->need;
+    const int need = p.ws.head->need;
     const bool over = p.ws.head->row_overflow != 0;
-    long long before, total;
-    free_before(p.ws, p.pool.chunks, blockIdx.x, &before, &total);
-    const bool ok = !over && need <= total;
-    if (blockIdx.x == 0 && tid == 0)
-        p.ws.head->status = (over ? row_bit : 0) | (need > total ? pool_bit : 0);
+    const uint2 f = free_before(p.ws, p.pool.chunks, chunk);
+    const bool enough = static_cast<unsigned>(need) <= f.y, ok = !over && enough;
+    if (chunk == 0 && tid == 0) p.ws.head->status = (over ? row_bit : 0) | (enough ? 0 : pool_bit);
 
     // tokens in pages that the row has already (and those that get no place)
-    const long long tokens = static_cast<long long>(p.rows) * p.L;
+    const unsigned tokens = static_cast<unsigned>(p.rows) * p.L, L = p.L;   // at most 2^28
     const int mask = (1 << p.shift) - 1;
-    for (long long t = static_cast<long long>(blockIdx.x) * THREADS + tid; t < tokens;
-         t += static_cast<long long>(gridDim.x) * THREADS) {
-        const int r = static_cast<int>(t / p.L), j = static_cast<int>(t % p.L);
+    for (unsigned t = blockIdx.x * THREADS + tid; t < tokens; t += gridDim.x * THREADS) {
+        const int r = static_cast<int>(t / L), j = static_cast<int>(t % L);
         const int len = p.ws.rows[r];
         const long long pos = len < 0 ? 0 : static_cast<long long>(len) + j;
         p.positions[t] = pos;
@@ -382,44 +427,32 @@ __global__ void __launch_bounds__(pg::THREADS)
         }
     }
     if (!ok) return;
-    if (blockIdx.x == 0)
+    if (chunk == 0)
         for (int r = tid; r < p.rows; r += THREADS)
             if (p.ws.rows[r] >= 0) p.lens[r] = p.ws.rows[r] + p.L;
 
     // fresh pages
-    if (static_cast<int>(blockIdx.x) >= p.pool.chunks) return;
-    const long long i0 = blockIdx.x * p.pool.chunk;
-    const long long i1 = i0 + p.pool.chunk < p.pool.num_pages ? i0 + p.pool.chunk : p.pool.num_pages;
-    for (long long i = i0; i < i1 && before < need; i += 4 * THREADS) {
-        const long long mine = i + 4 * tid;
-        const int4 v = mine < i1 ? refs4(p.pool, mine, 1) : make_int4(1, 1, 1, 1);
-        const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
-        int sum;
-        long long k = before + block_scan(f[0] + f[1] + f[2] + f[3], &sum);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (!f[u]) continue;
-            if (k < need) {
-                int lo = 0, hi = p.rows - 1;   // the last row whose prefix is at most k
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (p.ws.prefix[mid] <= k) lo = mid;
-                    else hi = mid - 1;
-                }
-                const int len = p.ws.rows[lo];
-                const long long page = mine + u;
-                const long long slot = ((static_cast<long long>(len) + mask) >> p.shift) + (k - p.ws.prefix[lo]);
-                p.table[static_cast<size_t>(lo) * p.max_pages + slot] = static_cast<int>(page);
-                p.pool.refs[page] = 1;
-                long long j = (slot << p.shift) - len;
-                if (j < 0) j = 0;
-                for (; j < p.L && ((len + j) >> p.shift) == slot; ++j)
-                    p.cache_loc[static_cast<long long>(lo) * p.L + j] = (page << p.shift) + ((len + j) & mask);
-            }
-            ++k;
-        }
-        before += sum;
+    if (!pool_block || f.x >= static_cast<unsigned>(need)) return;
+    for (int r = tid; r < p.rows; r += THREADS) {
+        s_prefix[r] = p.ws.prefix[r];
+        s_len[r] = p.ws.rows[r];
     }
+    __syncthreads();
+    hand_out(p.pool, chunk, bits, f.x, need, [&](long long page, long long k) {
+        int lo = 0, hi = p.rows - 1;   // the last row whose prefix is at most k
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_prefix[mid] <= k) lo = mid;
+            else hi = mid - 1;
+        }
+        const long long len = s_len[lo], slot = ((len + mask) >> p.shift) + (k - s_prefix[lo]);
+        p.table[static_cast<size_t>(lo) * p.max_pages + slot] = static_cast<int>(page);
+        p.pool.refs[page] = 1;
+        long long j = (slot << p.shift) - len;
+        if (j < 0) j = 0;
+        for (; j < p.L && ((len + j) >> p.shift) == slot; ++j)
+            p.cache_loc[static_cast<long long>(lo) * p.L + j] = (page << p.shift) + ((len + j) & mask);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -437,7 +470,7 @@ struct FreeParams {
 
 // One cluster per row: its blocks read the length, take turns at the entries
 // and, once all have read it, mark the row empty.
-__global__ void __cluster_dims__(pg::FREE_CLUSTER, 1, 1) __launch_bounds__(pg::THREADS)
+__global__ void __cluster_dims__(pg::FREE_CLUSTER, 1, 1) __launch_bounds__(pg::FREE_THREADS)
     free_kernel(const FreeParams p) {
     using namespace pg;
     const int r = blockIdx.x / FREE_CLUSTER, part = blockIdx.x % FREE_CLUSTER;
@@ -446,9 +479,14 @@ __global__ void __cluster_dims__(pg::FREE_CLUSTER, 1, 1) __launch_bounds__(pg::T
     cooperative_groups::this_cluster().sync();
     if (part == 0 && threadIdx.x == 0) p.lens[r] = -1;
     const int* row = p.table + static_cast<size_t>(r) * p.max_pages;
-    for (int j = part * THREADS + threadIdx.x; j < n; j += FREE_CLUSTER * THREADS) {
-        const int page = row[j];
-        if (page >= 0 && page < p.num_pages) atomicAdd(p.refs + page, -1);
+    constexpr int STRIDE = FREE_CLUSTER * FREE_THREADS;
+    for (long long j0 = part * FREE_THREADS + threadIdx.x; j0 < n; j0 += 4 * STRIDE) {
+        int page[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) page[u] = j0 + u * STRIDE < n ? row[j0 + u * STRIDE] : -1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (page[u] >= 0 && page[u] < p.num_pages) atomicAdd(p.refs + page[u], -1);
     }
 }
 
@@ -468,15 +506,8 @@ struct CompactParams {
 __global__ void __launch_bounds__(pg::THREADS) compact_count_kernel(const CompactParams p) {
     using namespace pg;
     pdl_launch_dependents();
-    const long long i0 = blockIdx.x * p.pool.chunk;
-    const long long i1 = i0 + p.pool.chunk < p.pool.num_pages ? i0 + p.pool.chunk : p.pool.num_pages;
-    long long n = 0;
-    for (long long i = i0 + 4 * threadIdx.x; i < i1; i += 4 * THREADS) {
-        const int4 r = refs4(p.pool, i, 1);
-        n += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
-    }
-    n = block_sum(n);
-    if (threadIdx.x == 0) p.ws.counts[blockIdx.x] = static_cast<int>(n);
+    const unsigned n = count_chunk(p.pool, blockIdx.x);
+    if (threadIdx.x == 0) p.ws.counts[blockIdx.x] = n;
 }
 
 // With `total` pages in use, the k-th page in use at or above `total` moves to
@@ -484,58 +515,53 @@ __global__ void __launch_bounds__(pg::THREADS) compact_count_kernel(const Compac
 // ranges of the pool, and no page moves that need not.
 __global__ void __launch_bounds__(pg::THREADS) compact_rank_kernel(const CompactParams p) {
     using namespace pg;
+    const int tid = threadIdx.x, chunk = blockIdx.x;
+    const long long i0 = chunk * p.pool.chunk, i1 = chunk_end(p.pool, chunk);
+    unsigned bits = free_bits(p.pool, i0 + RUN * tid, i1);   // the counts change in the next kernel only
     pdl_launch_dependents();
     pdl_wait_primary();
-    const int tid = threadIdx.x;
-    long long free_base, free_all;
-    free_before(p.ws, p.pool.chunks, blockIdx.x, &free_base, &free_all);
-    const long long total = p.pool.num_pages - free_all;
-    // free pages below `total` = pages that would move
-    long long holes, unused;
-    const int edge = static_cast<int>(total / p.pool.chunk);   // the chunk that `total` lies in
-    free_before(p.ws, p.pool.chunks, edge, &holes, &unused);
-    long long n = 0;
-    for (long long i = edge * p.pool.chunk + tid; i < total; i += THREADS) n += p.pool.refs[i] == 0;
-    holes += block_sum(n);
+    const uint2 f = free_before(p.ws, p.pool.chunks, chunk);
+    const long long total = p.pool.num_pages - f.y;
+    // holes: free pages below `total`, as many as pages that would move; the
+    // chunk that `total` lies in is counted up to it
+    const int edge = static_cast<int>(total / p.pool.chunk);
+    unsigned whole = 0, part = 0;
+    for (int i = tid; i < edge; i += THREADS) whole += p.ws.counts[i];
+    for (long long i = edge * p.pool.chunk + tid; i < total; i += THREADS) part += p.pool.refs[i] == 0;
+    const uint2 h = block_sum2(whole, part);
+    const long long holes = static_cast<long long>(h.x) + h.y, kept = total - holes;
     const int moves = static_cast<int>(holes < p.max_moves ? holes : p.max_moves);
-    if (blockIdx.x == 0 && tid == 0) {
+    if (chunk == 0 && tid == 0) {
         p.used[0] = static_cast<int>(total);
-        p.ws.head->total = total;
+        p.ws.head->total = static_cast<int>(total);
         p.ws.head->moves = moves;
         p.ws.head->status = 0;
     }
-    for (long long k = moves + static_cast<long long>(blockIdx.x) * THREADS + tid; k < p.max_moves;
+    for (long long k = moves + static_cast<long long>(chunk) * THREADS + tid; k < p.max_moves;
          k += static_cast<long long>(gridDim.x) * THREADS) {
         p.copy_src[k] = -1;
         p.copy_dst[k] = -1;
     }
-    // Pages in use below `total`: total - holes.
-    const long long kept = total - holes;
-    const long long i0 = blockIdx.x * p.pool.chunk;
-    const long long i1 = i0 + p.pool.chunk < p.pool.num_pages ? i0 + p.pool.chunk : p.pool.num_pages;
-    for (long long i = i0; i < i1; i += 4 * THREADS) {
-        const long long mine = i + 4 * tid;
-        const int4 v = mine < i1 ? refs4(p.pool, mine, 1) : make_int4(1, 1, 1, 1);
-        const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
+    long long before = f.x;   // free pages before the next ones
+    for (long long i = i0; i < i1; i += CHUNK) {
+        const long long mine = i + RUN * tid;
+        if (i != i0) bits = free_bits(p.pool, mine, i1);
         int sum;
-        long long k = free_base + block_scan(f[0] + f[1] + f[2] + f[3], &sum);
+        long long k = before + block_scan(__popc(bits), &sum);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < RUN; ++u) {
             const long long id = mine + u;
-            if (f[u]) {
+            if (bits >> u & 1) {
                 if (id < total && k < moves) p.copy_dst[k] = static_cast<int>(id);
+                if (id >= total) p.ws.rank[id] = -1;
                 ++k;
             } else if (id < i1 && id >= total) {
                 const long long m = id - k - kept;   // id - k pages in use come before this one
-                if (m < moves) {
-                    p.copy_src[m] = static_cast<int>(id);
-                    p.ws.rank[id] = static_cast<int>(m);
-                } else {
-                    p.ws.rank[id] = -1;
-                }
+                if (m < moves) p.copy_src[m] = static_cast<int>(id);
+                p.ws.rank[id] = m < moves ? static_cast<int>(m) : -1;
             }
         }
-        free_base += sum;
+        before += sum;
     }
 }
 
@@ -543,27 +569,30 @@ __global__ void __launch_bounds__(pg::THREADS) compact_rank_kernel(const Compact
 // the counts.
 __global__ void __launch_bounds__(pg::THREADS) compact_apply_kernel(const CompactParams p) {
     using namespace pg;
+    const bool counts = static_cast<int>(blockIdx.y) == p.rows;
+    const int n = counts ? 0 : pages_of(p.lens[blockIdx.y], p.shift, p.max_pages);
+    const long long stride = static_cast<long long>(gridDim.x) * THREADS, j00 = blockIdx.x * THREADS + threadIdx.x;
     pdl_wait_primary();
-    const int moves = p.ws.head->moves;
-    const long long total = p.ws.head->total;
-    if (static_cast<int>(blockIdx.y) == p.rows) {
-        for (int k = blockIdx.x * THREADS + threadIdx.x; k < moves; k += gridDim.x * THREADS) {
+    if (counts) {
+        const int moves = p.ws.head->moves;
+        for (long long k = j00; k < moves; k += stride) {
             const int s = p.copy_src[k], d = p.copy_dst[k];
             p.pool.refs[d] = p.pool.refs[s];
             p.pool.refs[s] = 0;
         }
         return;
     }
-    const int n = pages_of(p.lens[blockIdx.y], p.shift, p.max_pages);
+    const int total = p.ws.head->total;
     int* row = p.table + static_cast<size_t>(blockIdx.y) * p.max_pages;
-    for (long long j = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x; j < n;
-         j += static_cast<long long>(gridDim.x) * THREADS) {
-        const int page = row[j];
-        if (page >= total && page < p.pool.num_pages) {
-            const int k = p.ws.rank[page];
-            // an entry whose page is free has no rank of this call: it stays
-            if (k >= 0 && k < moves && p.copy_src[k] == page) row[j] = p.copy_dst[k];
-        }
+    for (long long j0 = j00; j0 < n; j0 += 4 * stride) {   // four chains of loads at a time
+        int page[4], k[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) page[u] = j0 + u * stride < n ? row[j0 + u * stride] : -1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) k[u] = page[u] >= total && page[u] < p.pool.num_pages ? p.ws.rank[page[u]] : -1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (k[u] >= 0) row[j0 + u * stride] = p.copy_dst[k[u]];
     }
 }
 
@@ -574,41 +603,50 @@ __global__ void __launch_bounds__(pg::THREADS) compact_apply_kernel(const Compac
 struct CopyParams {
     uint8_t* cache[pg::MAX_CACHES];
     const int *src, *dst;
-    int n, chunks, lanes;      // 16-byte chunks per page, threads per page (a power of two)
+    int caches, n;
+    int chunks, lanes;         // 16-byte chunks per page, threads per page (a power of two)
     long long num_pages;
     size_t page_bytes;
 };
 
-// A page is copied by `lanes` threads, 16 bytes each at a time, four loads of
-// a thread in flight before its stores: over four pairs when a page is one
-// chunk a thread (WIDE false), else over four chunks of one pair.
+// A page is copied by `lanes` threads, 16 bytes each at a time, several loads of
+// a thread in flight before its stores: over four pairs in two caches when a
+// page is one chunk a thread (WIDE false: K and V rows of single-token pages),
+// else over four chunks of one pair in one cache.
 template <bool WIDE>
 __global__ void __launch_bounds__(pg::THREADS) pages_copy_kernel(const CopyParams p) {
     using namespace pg;
     const int lane = threadIdx.x % p.lanes, group = threadIdx.x / p.lanes, groups = THREADS / p.lanes;
-    uint8_t* cache = p.cache[blockIdx.y];
     if (!WIDE) {
+        uint8_t* c0 = p.cache[2 * blockIdx.y];
+        uint8_t* c1 = 2 * blockIdx.y + 1 < p.caches ? p.cache[2 * blockIdx.y + 1] : nullptr;
         for (long long i0 = static_cast<long long>(blockIdx.x) * groups * 4 + group; i0 < p.n;
              i0 += static_cast<long long>(gridDim.x) * groups * 4) {
-            uint4 v[4];
-            uint4* to[4];
+            int s[4], d[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const long long i = i0 + static_cast<long long>(u) * groups;
-                to[u] = nullptr;
-                if (i < p.n && lane < p.chunks) {
-                    const int s = p.src[i], d = p.dst[i];
-                    if (s >= 0 && d >= 0 && s < p.num_pages && d < p.num_pages) {
-                        v[u] = reinterpret_cast<const uint4*>(cache + s * p.page_bytes)[lane];
-                        to[u] = reinterpret_cast<uint4*>(cache + d * p.page_bytes) + lane;
-                    }
-                }
+                const bool in = i < p.n && lane < p.chunks;
+                s[u] = in ? p.src[i] : -1;
+                d[u] = in ? p.dst[i] : -1;
+                if (d[u] < 0 || s[u] >= p.num_pages || d[u] >= p.num_pages) s[u] = -1;
             }
+            uint4 v[4], w[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (to[u] != nullptr) *to[u] = v[u];
+                if (s[u] >= 0) {
+                    v[u] = reinterpret_cast<const uint4*>(c0 + s[u] * p.page_bytes)[lane];
+                    if (c1 != nullptr) w[u] = reinterpret_cast<const uint4*>(c1 + s[u] * p.page_bytes)[lane];
+                }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (s[u] >= 0) {
+                    reinterpret_cast<uint4*>(c0 + d[u] * p.page_bytes)[lane] = v[u];
+                    if (c1 != nullptr) reinterpret_cast<uint4*>(c1 + d[u] * p.page_bytes)[lane] = w[u];
+                }
         }
     } else {
+        uint8_t* cache = p.cache[blockIdx.y];
         for (long long i = static_cast<long long>(blockIdx.x) * groups + group; i < p.n;
              i += static_cast<long long>(gridDim.x) * groups) {
             const int s = p.src[i], d = p.dst[i];

@@ -86,11 +86,11 @@ int check_device() {
 }
 
 template <class... Params, class... Args>
-int launch(const char* name, void (*kern)(Params...), dim3 grid, int threads, cudaStream_t s, bool pdl, Args... args) {
+int launch(const char* name, void (*kern)(Params...), dim3 grid, cudaStream_t s, bool pdl, Args... args) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = dim3(gad::pg::THREADS);
     cfg.stream = s;
     cudaLaunchAttribute attr = pdl_attr();
     cfg.attrs = &attr;
@@ -99,8 +99,6 @@ int launch(const char* name, void (*kern)(Params...), dim3 grid, int threads, cu
     if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(e));
     return GAD_OK;
 }
-
-constexpr int kThreads = gad::pg::THREADS;
 
 int shift_of(int page_size) { return page_size == 64 ? 6 : 0; }
 
@@ -157,7 +155,7 @@ int gad_pages_copy(void* const* caches, int n_caches, size_t page_bytes, int64_t
         for (int i = 0; i < m; ++i) p.cache[i] = static_cast<uint8_t*>(caches[c0 + i]);
         p.caches = m;
         const dim3 grid(gx, static_cast<unsigned>(wide ? m : (m + 1) / 2));
-        st = launch("page copy", wide ? gad::pages_copy_kernel<true> : gad::pages_copy_kernel<false>, grid, kThreads,
+        st = launch("page copy", wide ? gad::pages_copy_kernel<true> : gad::pages_copy_kernel<false>, grid,
                     static_cast<cudaStream_t>(stream), false, p);
         if (st != GAD_OK) return st;
     }
@@ -205,11 +203,11 @@ int gad_pages_fork(const int32_t* page_table, const int32_t* lens, int rows_in, 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = max_pages % 4 == 0 && aligned(page_table, 16) && aligned(out_table, 16);
     const dim3 grid(blocks(max_pages, gad::pg::COLS), blocks(rows_in > rows_out ? rows_in : rows_out, gad::pg::ROWS));
-    st = launch("fork", vec ? gad::fork_kernel<true> : gad::fork_kernel<false>, grid, kThreads, s, false, p);
+    st = launch("fork", vec ? gad::fork_kernel<true> : gad::fork_kernel<false>, grid, s, false, p);
     if (st != GAD_OK || page_size == 1) return st;   // single-token pages are never partly filled
-    st = launch("fork count", gad::fork_count_kernel, dim3(p.pool.chunks + 1), kThreads, s, true, p);
+    st = launch("fork count", gad::fork_count_kernel, dim3(p.pool.chunks + 1), s, true, p);
     if (st != GAD_OK) return st;
-    return launch("fork assign", gad::fork_assign_kernel, dim3(p.pool.chunks), kThreads, s, true, p,
+    return launch("fork assign", gad::fork_assign_kernel, dim3(p.pool.chunks), s, true, p,
                   static_cast<int>(GAD_STATUS_PAGES_POOL));
 }
 
@@ -242,13 +240,13 @@ int gad_pages_extend(int32_t* page_table, int32_t* lens, int rows, int L, int ma
     p.pool = bind_pool(refs, num_pages);
     p.ws = bind_ws(workspace, num_pages);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = launch("extend count", gad::extend_count_kernel, dim3(p.pool.chunks + 1), kThreads, s, false, p);
+    st = launch("extend count", gad::extend_count_kernel, dim3(p.pool.chunks + 1), s, false, p);
     if (st != GAD_OK) return st;
     // enough blocks for the tokens' rows too
     const long long tok = (static_cast<long long>(rows) * L + 8 * gad::pg::THREADS - 1) / (8 * gad::pg::THREADS);
     const long long grid = tok > 1024 ? 1024 : tok;
     return launch("extend assign", gad::extend_assign_kernel,
-                  dim3(static_cast<unsigned>(grid > p.pool.chunks ? grid : p.pool.chunks)), kThreads, s, true, p,
+                  dim3(static_cast<unsigned>(grid > p.pool.chunks ? grid : p.pool.chunks)), s, true, p,
                   static_cast<int>(GAD_STATUS_PAGES_POOL), static_cast<int>(GAD_STATUS_PAGES_ROW));
 }
 
@@ -272,8 +270,28 @@ int gad_pages_free(const int32_t* page_table, int32_t* lens, int rows, const uin
     p.shift = shift_of(page_size);
     p.refs = refs;
     p.num_pages = num_pages;
-    return launch("free", gad::free_kernel, dim3(static_cast<unsigned>(rows) * gad::pg::FREE_CLUSTER),
-                  gad::pg::FREE_THREADS, static_cast<cudaStream_t>(stream), false, p);
+    // four entries a thread: blocks of up to 1024 threads, up to eight of them
+    // (the portable cluster size) per row
+    int threads = 64;
+    while (threads < 1024 && threads * 4 < max_pages) threads *= 2;
+    p.parts = 1;
+    while (p.parts < 8 && static_cast<long long>(p.parts) * threads * 4 < max_pages) p.parts *= 2;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(rows) * p.parts);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr;
+    std::memset(&attr, 0, sizeof(attr));
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.parts;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, gad::free_kernel, p);
+    if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "free launch: %s", cudaGetErrorString(e));
+    return GAD_OK;
 }
 
 int gad_pages_compact(int32_t* page_table, const int32_t* lens, int rows, int max_pages, int page_size, int32_t* refs,
@@ -306,13 +324,13 @@ int gad_pages_compact(int32_t* page_table, const int32_t* lens, int rows, int ma
     p.pool = bind_pool(refs, num_pages);
     p.ws = bind_ws(workspace, num_pages);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = launch("compact count", gad::compact_count_kernel, dim3(p.pool.chunks), kThreads, s, false, p);
+    st = launch("compact count", gad::compact_count_kernel, dim3(p.pool.chunks), s, false, p);
     if (st != GAD_OK) return st;
-    st = launch("compact rank", gad::compact_rank_kernel, dim3(p.pool.chunks), kThreads, s, true, p);
+    st = launch("compact rank", gad::compact_rank_kernel, dim3(p.pool.chunks), s, true, p);
     if (st != GAD_OK) return st;
     const unsigned gx = blocks(max_pages, 4 * gad::pg::THREADS);
     return launch("compact apply", gad::compact_apply_kernel,
-                  dim3(gx < 1024 ? gx : 1024, static_cast<unsigned>(rows) + 1), kThreads, s, true, p);
+                  dim3(gx < 1024 ? gx : 1024, static_cast<unsigned>(rows) + 1), s, true, p);
 }
 
 }  // extern "C"

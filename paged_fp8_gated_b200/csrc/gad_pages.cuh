@@ -32,8 +32,7 @@ constexpr int MAX_ROWS = 4096;
 constexpr int COLS = 4 * THREADS;    // fork: table columns per block, four a thread
 constexpr int ROWS = 8;              // fork: table rows per block
 constexpr int RUN = CHUNK / THREADS; // pages of a chunk that a thread looks at
-constexpr int FREE_CLUSTER = 8;      // blocks that share a row in free_kernel
-constexpr int FREE_THREADS = 1024;
+constexpr int EARLY_CHUNKS = 16;
 constexpr int MAX_CACHES = 64;       // caches per copy launch
 
 // Pages per chunk: CHUNK, or the smallest multiple of it with at most MAX_CHUNKS chunks.
@@ -235,6 +234,12 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
             for (int u = 0; u < 4; ++u) e[u] = col(u) < n ? row[col(u)] : -1;
         }
     };
+    int e[ROWS][4];   // all rows' entries at a time
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        const int n = s_kids[k] == 1 ? 0 : pages_of(s_len[k], p.shift, p.max_pages);
+        entries(e[k], p.table + static_cast<size_t>(y0 + k) * p.max_pages, n);
+    }
     int page[4] = {-1, -1, -1, -1}, left[4] = {0, 0, 0, 0};
     auto flush = [&](int u) {
         if (left[u] != 0 && page[u] >= 0 && page[u] < p.pool.num_pages) atomicAdd(p.pool.refs + page[u], left[u]);
@@ -242,18 +247,15 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
         const int kids = s_kids[k], len = s_len[k];
-        const int n = pages_of(len, p.shift, p.max_pages);
-        if (kids == 1 || n <= c0) continue;
+        const int n = kids == 1 ? 0 : pages_of(len, p.shift, p.max_pages);
         const int last = has_partial(len, p.shift, p.max_pages) ? n - 1 : -1;
-        int e[4];
-        entries(e, p.table + static_cast<size_t>(y0 + k) * p.max_pages, n);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             if (col(u) >= n) continue;
             const int d = (col(u) == last ? min(kids, 1) : kids) - 1;
-            if (e[u] != page[u]) {
+            if (e[k][u] != page[u]) {
                 flush(u);
-                page[u] = e[u];
+                page[u] = e[k][u];
                 left[u] = 0;
             }
             left[u] += d;
@@ -262,30 +264,32 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) flush(u);
 
+    auto taken = [&](int k) {   // entries that new row y0 + k takes over
+        const bool fresh = s_elder[k] && has_partial(s_new[k], p.shift, p.max_pages);
+        return pages_of(s_new[k], p.shift, p.max_pages) - fresh;
+    };
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k)
+        entries(e[k], p.table + static_cast<size_t>(s_par[k] >= 0 ? s_par[k] : 0) * p.max_pages, taken(k));
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
-        const int y = y0 + k, len = s_new[k];
-        if (y >= p.rows_out) break;
-        const bool fresh = s_elder[k] && has_partial(len, p.shift, p.max_pages);
-        const int n = pages_of(len, p.shift, p.max_pages) - fresh;
-        if (blockIdx.x == 0 && tid == 0) {
-            p.out_lens[y] = len < 0 ? -1 : len;
-            p.copy_src[y] = -1;
-            p.copy_dst[y] = -1;
-            p.ws.rows[y] = fresh;
-            if (y == 0) p.ws.head->status = 0;
-        }
-        if (n <= c0) continue;
-        int e[4];
-        entries(e, p.table + static_cast<size_t>(s_par[k]) * p.max_pages, n);
+        const int y = y0 + k, n = taken(k);
         int* dst = p.out_table + static_cast<size_t>(y) * p.max_pages;
         if (VEC && col(3) < n) {
-            *reinterpret_cast<int4*>(dst + col(0)) = make_int4(e[0], e[1], e[2], e[3]);
+            *reinterpret_cast<int4*>(dst + col(0)) = make_int4(e[k][0], e[k][1], e[k][2], e[k][3]);
         } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (col(u) < n) dst[col(u)] = e[u];
+                if (col(u) < n) dst[col(u)] = e[k][u];
         }
+    }
+    if (blockIdx.x == 0 && tid < ROWS && y0 + tid < p.rows_out) {
+        const int y = y0 + tid, len = s_new[tid];
+        p.out_lens[y] = len < 0 ? -1 : len;
+        p.copy_src[y] = -1;
+        p.copy_dst[y] = -1;
+        p.ws.rows[y] = s_elder[tid] && has_partial(len, p.shift, p.max_pages);
+        if (y == 0) p.ws.head->status = 0;
     }
 }
 
@@ -399,9 +403,11 @@ __global__ void __launch_bounds__(pg::THREADS)
     __shared__ int s_prefix[MAX_ROWS], s_len[MAX_ROWS];
     const int tid = threadIdx.x, chunk = blockIdx.x;
     const bool pool_block = chunk < p.pool.chunks;
-    // the counts change in this kernel only, a chunk by its own block
-    const unsigned bits =
-        pool_block ? free_bits(p.pool, chunk * p.pool.chunk + RUN * tid, chunk_end(p.pool, chunk)) : 0;
+    // The counts change in this kernel only, a chunk by its own block.  Pages are
+    // usually found in the first chunks, which look early.
+    unsigned bits = 0;
+    auto look = [&] { bits = free_bits(p.pool, chunk * p.pool.chunk + RUN * tid, chunk_end(p.pool, chunk)); };
+    if (pool_block && chunk < EARLY_CHUNKS) look();
     pdl_wait_primary();
     const int need = p.ws.head->need;
     const bool over = p.ws.head->row_overflow != 0;
@@ -433,6 +439,7 @@ __global__ void __launch_bounds__(pg::THREADS)
 
     // fresh pages
     if (!pool_block || f.x >= static_cast<unsigned>(need)) return;
+    if (chunk >= EARLY_CHUNKS) look();
     for (int r = tid; r < p.rows; r += THREADS) {
         s_prefix[r] = p.ws.prefix[r];
         s_len[r] = p.ws.rows[r];
@@ -463,27 +470,26 @@ struct FreeParams {
     const int* table;
     int* lens;
     const uint8_t* leave;
-    int rows, max_pages, shift;
+    int rows, max_pages, shift, parts;
     int* refs;
     long long num_pages;
 };
 
-// One cluster per row: its blocks read the length, take turns at the entries
-// and, once all have read it, mark the row empty.
-__global__ void __cluster_dims__(pg::FREE_CLUSTER, 1, 1) __launch_bounds__(pg::FREE_THREADS)
-    free_kernel(const FreeParams p) {
+// One cluster of `parts` blocks per row: they read the length, take turns at
+// the entries and, once all have read it, mark the row empty.
+__global__ void free_kernel(const FreeParams p) {
     using namespace pg;
-    const int r = blockIdx.x / FREE_CLUSTER, part = blockIdx.x % FREE_CLUSTER;
+    const int r = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
     if (p.leave != nullptr && p.leave[r] == 0) return;   // the whole cluster
     const int n = pages_of(p.lens[r], p.shift, p.max_pages);
     cooperative_groups::this_cluster().sync();
     if (part == 0 && threadIdx.x == 0) p.lens[r] = -1;
     const int* row = p.table + static_cast<size_t>(r) * p.max_pages;
-    constexpr int STRIDE = FREE_CLUSTER * FREE_THREADS;
-    for (long long j0 = part * FREE_THREADS + threadIdx.x; j0 < n; j0 += 4 * STRIDE) {
+    const long long stride = static_cast<long long>(p.parts) * blockDim.x;
+    for (long long j0 = static_cast<long long>(part) * blockDim.x + threadIdx.x; j0 < n; j0 += 4 * stride) {
         int page[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) page[u] = j0 + u * STRIDE < n ? row[j0 + u * STRIDE] : -1;
+        for (int u = 0; u < 4; ++u) page[u] = j0 + u * stride < n ? row[j0 + u * stride] : -1;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             if (page[u] >= 0 && page[u] < p.num_pages) atomicAdd(p.refs + page[u], -1);

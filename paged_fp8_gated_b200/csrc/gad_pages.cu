@@ -86,11 +86,11 @@ int check_device() {
 }
 
 template <class... Params, class... Args>
-int launch(const char* name, void (*kern)(Params...), dim3 grid, cudaStream_t s, bool pdl, Args... args) {
+int launch(const char* name, void (*kern)(Params...), dim3 grid, int threads, cudaStream_t s, bool pdl, Args... args) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(gad::pg::THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.stream = s;
     cudaLaunchAttribute attr = pdl_attr();
     cfg.attrs = &attr;
@@ -99,6 +99,13 @@ int launch(const char* name, void (*kern)(Params...), dim3 grid, cudaStream_t s,
     if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(e));
     return GAD_OK;
 }
+
+constexpr int T = gad::pg::THREADS;
+// Most tokens that extend's one block for a small pool places.
+constexpr long long kSmallTokens = 16384;
+
+// Whether a kernel of one block looks through the pool.
+bool small_pool(int64_t num_pages) { return num_pages <= gad::pg::SMALL_POOL; }
 
 int shift_of(int page_size) { return page_size == 64 ? 6 : 0; }
 
@@ -147,15 +154,15 @@ int gad_pages_copy(void* const* caches, int n_caches, size_t page_bytes, int64_t
     const bool wide = p.chunks >= 128;
     const int want = wide ? (p.chunks + 3) / 4 : p.chunks;
     p.lanes = 1;
-    while (p.lanes < want && p.lanes < gad::pg::THREADS) p.lanes *= 2;
-    const long long per_block = (gad::pg::THREADS / p.lanes) * (wide ? 1 : 4);
+    while (p.lanes < want && p.lanes < T) p.lanes *= 2;
+    const long long per_block = (T / p.lanes) * (wide ? 1 : 4);
     const unsigned gx = blocks(n, per_block) < (1u << 20) ? blocks(n, per_block) : (1u << 20);
     for (int c0 = 0; c0 < n_caches; c0 += gad::pg::MAX_CACHES) {
         const int m = n_caches - c0 < gad::pg::MAX_CACHES ? n_caches - c0 : gad::pg::MAX_CACHES;
         for (int i = 0; i < m; ++i) p.cache[i] = static_cast<uint8_t*>(caches[c0 + i]);
         p.caches = m;
         const dim3 grid(gx, static_cast<unsigned>(wide ? m : (m + 1) / 2));
-        st = launch("page copy", wide ? gad::pages_copy_kernel<true> : gad::pages_copy_kernel<false>, grid,
+        st = launch("page copy", wide ? gad::pages_copy_kernel<true> : gad::pages_copy_kernel<false>, grid, T,
                     static_cast<cudaStream_t>(stream), false, p);
         if (st != GAD_OK) return st;
     }
@@ -203,12 +210,14 @@ int gad_pages_fork(const int32_t* page_table, const int32_t* lens, int rows_in, 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = max_pages % 4 == 0 && aligned(page_table, 16) && aligned(out_table, 16);
     const dim3 grid(blocks(max_pages, gad::pg::COLS), blocks(rows_in > rows_out ? rows_in : rows_out, gad::pg::ROWS));
-    st = launch("fork", vec ? gad::fork_kernel<true> : gad::fork_kernel<false>, grid, s, false, p);
+    st = launch("fork", vec ? gad::fork_kernel<true> : gad::fork_kernel<false>, grid, T, s, false, p);
     if (st != GAD_OK || page_size == 1) return st;   // single-token pages are never partly filled
-    st = launch("fork count", gad::fork_count_kernel, dim3(p.pool.chunks + 1), s, true, p);
+    const int pool_bit = GAD_STATUS_PAGES_POOL;
+    if (small_pool(num_pages))
+        return launch("fork assign", gad::fork_assign_small_kernel, dim3(1), gad::pg::ONE_THREADS, s, true, p, pool_bit);
+    st = launch("fork count", gad::fork_count_kernel, dim3(p.pool.chunks + 1), T, s, true, p);
     if (st != GAD_OK) return st;
-    return launch("fork assign", gad::fork_assign_kernel, dim3(p.pool.chunks), s, true, p,
-                  static_cast<int>(GAD_STATUS_PAGES_POOL));
+    return launch("fork assign", gad::fork_assign_kernel, dim3(p.pool.chunks), T, s, true, p, pool_bit);
 }
 
 int gad_pages_extend(int32_t* page_table, int32_t* lens, int rows, int L, int max_pages, int page_size, int32_t* refs,
@@ -240,14 +249,18 @@ int gad_pages_extend(int32_t* page_table, int32_t* lens, int rows, int L, int ma
     p.pool = bind_pool(refs, num_pages);
     p.ws = bind_ws(workspace, num_pages);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = launch("extend count", gad::extend_count_kernel, dim3(p.pool.chunks + 1), s, false, p);
+    const int pool_bit = GAD_STATUS_PAGES_POOL, row_bit = GAD_STATUS_PAGES_ROW;
+    const long long tokens = static_cast<long long>(rows) * L;
+    if (small_pool(num_pages) && tokens <= kSmallTokens)
+        return launch("extend", gad::extend_small_kernel, dim3(1), gad::pg::ONE_THREADS, s, false, p, pool_bit, row_bit);
+    st = launch("extend count", gad::extend_count_kernel, dim3(p.pool.chunks + 1), T, s, false, p);
     if (st != GAD_OK) return st;
     // enough blocks for the tokens' rows too
-    const long long tok = (static_cast<long long>(rows) * L + 8 * gad::pg::THREADS - 1) / (8 * gad::pg::THREADS);
+    const long long tok = (tokens + 8 * T - 1) / (8 * T);
     const long long grid = tok > 1024 ? 1024 : tok;
     return launch("extend assign", gad::extend_assign_kernel,
-                  dim3(static_cast<unsigned>(grid > p.pool.chunks ? grid : p.pool.chunks)), s, true, p,
-                  static_cast<int>(GAD_STATUS_PAGES_POOL), static_cast<int>(GAD_STATUS_PAGES_ROW));
+                  dim3(static_cast<unsigned>(grid > p.pool.chunks ? grid : p.pool.chunks)), T, s, true, p, pool_bit,
+                  row_bit);
 }
 
 int gad_pages_free(const int32_t* page_table, int32_t* lens, int rows, const uint8_t* leave, int max_pages,
@@ -324,13 +337,17 @@ int gad_pages_compact(int32_t* page_table, const int32_t* lens, int rows, int ma
     p.pool = bind_pool(refs, num_pages);
     p.ws = bind_ws(workspace, num_pages);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = launch("compact count", gad::compact_count_kernel, dim3(p.pool.chunks), s, false, p);
+    if (small_pool(num_pages)) {
+        st = launch("compact", gad::compact_small_kernel, dim3(1), gad::pg::ONE_THREADS, s, false, p);
+    } else {
+        st = launch("compact count", gad::compact_count_kernel, dim3(p.pool.chunks), T, s, false, p);
+        if (st != GAD_OK) return st;
+        st = launch("compact rank", gad::compact_rank_kernel, dim3(p.pool.chunks), T, s, true, p);
+    }
     if (st != GAD_OK) return st;
-    st = launch("compact rank", gad::compact_rank_kernel, dim3(p.pool.chunks), s, true, p);
-    if (st != GAD_OK) return st;
-    const unsigned gx = blocks(max_pages, 4 * gad::pg::THREADS);
+    const unsigned gx = blocks(max_pages, 4 * T);
     return launch("compact apply", gad::compact_apply_kernel,
-                  dim3(gx < 1024 ? gx : 1024, static_cast<unsigned>(rows) + 1), s, true, p);
+                  dim3(gx < 1024 ? gx : 1024, static_cast<unsigned>(rows) + 1), T, s, true, p);
 }
 
 }  // extern "C"

@@ -13,8 +13,9 @@
 // Handing out pages needs the k-th free page for k = 0, 1, ...: one pass counts
 // the free pages per chunk of the pool, a second one ranks the free pages of
 // each chunk behind the sum of the chunks before it and gives each to its row.
-// Both read the counts once (4 bytes a page).  Page ids outside [0, num_pages)
-// are skipped everywhere.
+// Both read the counts once (4 bytes a page).  A pool of at most SMALL_POOL pages
+// is looked at by one block, which keeps the free pages as bits between the two
+// and saves a launch.  Page ids outside [0, num_pages) are skipped everywhere.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -32,7 +33,10 @@ constexpr int MAX_ROWS = 4096;
 constexpr int COLS = 4 * THREADS;    // fork: table columns per block, four a thread
 constexpr int ROWS = 8;              // fork: table rows per block
 constexpr int RUN = CHUNK / THREADS; // pages of a chunk that a thread looks at
-constexpr int EARLY_CHUNKS = 16;
+constexpr int EARLY_CHUNKS = 16;     // chunks that extend looks at before it knows that it must
+constexpr int ONE_THREADS = 1024;    // threads of a kernel of one block
+constexpr int SMALL_POOL = 64 * ONE_THREADS;
+constexpr int LIST = 2048;           // free pages that are handed out at a time
 constexpr int MAX_CACHES = 64;       // caches per copy launch
 
 // Pages per chunk: CHUNK, or the smallest multiple of it with at most MAX_CHUNKS chunks.
@@ -77,9 +81,10 @@ __device__ __forceinline__ bool has_partial(int len, int shift, int max_pages) {
     return ((static_cast<long long>(len) + (1 << shift) - 1) >> shift) <= max_pages;
 }
 
-// Exclusive prefix of v over the block's threads; *total gets the sum.
+// Exclusive prefix of v over the block's T threads; *total gets the sum.
+template <int T>
 __device__ __forceinline__ int block_scan(int v, int* total) {
-    __shared__ int warp_sum[THREADS / 32];
+    __shared__ int warp_sum[T / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
@@ -90,31 +95,23 @@ __device__ __forceinline__ int block_scan(int v, int* total) {
     __syncthreads();  // the previous call's readers are done
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        const int s = warp_sum[w];
-        if (w < warp) before += s;
-        all += s;
-    }
-    *total = all;
+    const int s = lane < T / 32 ? warp_sum[lane] : 0;   // every warp adds the warps' sums up
+    *total = __reduce_add_sync(0xffffffffu, s);
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? s : 0);
     return before + x - v;
 }
-// Sums of a and b over the block's threads (below 2^32).
+// Sums of a and b over the block's T threads (below 2^32).
+template <int T>
 __device__ __forceinline__ uint2 block_sum2(unsigned a, unsigned b) {
-    __shared__ uint2 warp_sum[THREADS / 32];
+    __shared__ uint2 warp_sum[T / 32];
+    const int lane = threadIdx.x & 31;
     a = __reduce_add_sync(0xffffffffu, a);
     b = __reduce_add_sync(0xffffffffu, b);
     __syncthreads();  // the previous call's readers are done
-    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = make_uint2(a, b);
+    if (lane == 0) warp_sum[threadIdx.x >> 5] = make_uint2(a, b);
     __syncthreads();
-    uint2 s = make_uint2(0, 0);
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        s.x += warp_sum[w].x;
-        s.y += warp_sum[w].y;
-    }
-    return s;
+    const uint2 s = lane < T / 32 ? warp_sum[lane] : make_uint2(0, 0);
+    return make_uint2(__reduce_add_sync(0xffffffffu, s.x), __reduce_add_sync(0xffffffffu, s.y));
 }
 
 // Four counts from page i on (i a multiple of 4); pages past the pool count as
@@ -128,14 +125,15 @@ __device__ __forceinline__ int4 refs4(const Pool& p, long long i, int past) {
     return r;
 }
 
-// Which of the RUN pages from i on are free, as bits (i a multiple of 4).
-__device__ __forceinline__ unsigned free_bits(const Pool& p, long long i, long long end) {
-    unsigned bits = 0;
+// Which of the `run` pages from i on are free, as bits (i and run multiples of
+// 4, run at most MAX_RUN).
+template <int MAX_RUN>
+__device__ __forceinline__ uint64_t free_bits(const Pool& p, long long i, long long end, int run) {
+    uint64_t bits = 0;
 #pragma unroll
-    for (int u = 0; u < RUN / 4; ++u) {
-        const long long at = i + 4 * u;
-        const int4 r = at < end ? refs4(p, at, 1) : make_int4(1, 1, 1, 1);
-        bits |= static_cast<unsigned>((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << 4 * u;
+    for (int u = 0; u < MAX_RUN; u += 4) {
+        const int4 r = u < run && i + u < end ? refs4(p, i + u, 1) : make_int4(1, 1, 1, 1);
+        bits |= static_cast<uint64_t>((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << u;
     }
     return bits;
 }
@@ -147,8 +145,9 @@ __device__ __forceinline__ long long chunk_end(const Pool& p, int chunk) {
 __device__ __forceinline__ unsigned count_chunk(const Pool& p, int chunk) {
     const long long end = chunk_end(p, chunk);
     unsigned n = 0;
-    for (long long i = chunk * p.chunk + RUN * threadIdx.x; i < end; i += CHUNK) n += __popc(free_bits(p, i, end));
-    return block_sum2(n, 0).x;
+    for (long long i = chunk * p.chunk + RUN * threadIdx.x; i < end; i += CHUNK)
+        n += __popcll(free_bits<RUN>(p, i, end, RUN));
+    return block_sum2<THREADS>(n, 0).x;
 }
 // Free pages in the chunks before `chunk` (x), and in all of them (y).
 __device__ __forceinline__ uint2 free_before(const Ws& ws, int chunks, int chunk) {
@@ -158,22 +157,54 @@ __device__ __forceinline__ uint2 free_before(const Ws& ws, int chunks, int chunk
         t += c;
         if (i < chunk) b += c;
     }
-    return block_sum2(b, t);
+    return block_sum2<THREADS>(b, t);
 }
-// give(page, k) for the free pages of a chunk whose rank k is below `need`;
-// `before`: free pages before the chunk; `bits`: free_bits of its first CHUNK pages.
+
+// give(page, before + q) for the first n free pages of a block's stretch of the
+// pool, q = 0 .. n - 1: a thread's free pages are `bits` from page `mine` on,
+// `rank` of the stretch's come before them.  The pages go through shared memory
+// so that all threads give (a give is a chain of loads).
+template <int T, class F>
+__device__ __forceinline__ void hand_out(uint64_t bits, long long mine, int rank, int n, long long before, F give) {
+    __shared__ int s_list[LIST];
+    for (int lo = 0; lo < n; lo += LIST) {
+        __syncthreads();
+        int q = rank - lo;
+        for (uint64_t b = bits; b != 0 && q < LIST; ++q, b &= b - 1)
+            if (q >= 0) s_list[q] = static_cast<int>(mine + __ffsll(b) - 1);
+        __syncthreads();
+        const int m = n - lo < LIST ? n - lo : LIST;
+        for (int i = threadIdx.x; i < m; i += T) give(static_cast<long long>(s_list[i]), before + lo + i);
+    }
+}
+// The same for a chunk, `before` free pages in the chunks before it, ranks below
+// `need`; `bits`: those of its first CHUNK pages.
 template <class F>
-__device__ __forceinline__ void hand_out(const Pool& p, int chunk, unsigned bits, long long before, long long need,
-                                         F give) {
+__device__ __forceinline__ void hand_out_chunk(const Pool& p, int chunk, uint64_t bits, long long before, long long need,
+                                               F give) {
     const long long end = chunk_end(p, chunk);
     for (long long i0 = chunk * p.chunk; i0 < end && before < need; i0 += CHUNK) {
         const long long mine = i0 + RUN * threadIdx.x;
-        if (i0 != chunk * p.chunk) bits = mine < end ? free_bits(p, mine, end) : 0;
+        if (i0 != chunk * p.chunk) bits = mine < end ? free_bits<RUN>(p, mine, end, RUN) : 0;
         int sum;
-        long long k = before + block_scan(__popc(bits), &sum);
-        for (; bits != 0 && k < need; ++k, bits &= bits - 1) give(mine + __ffs(bits) - 1, k);
+        const int rank = block_scan<THREADS>(__popcll(bits), &sum);
+        hand_out<THREADS>(bits, mine, rank, static_cast<int>(sum < need - before ? sum : need - before), before, give);
         before += sum;
     }
+}
+// A pool of at most SMALL_POOL pages as one block sees it.
+struct Small {
+    uint64_t bits;     // the thread's free pages from page `mine` on
+    long long mine;
+    int rank, total;   // free pages before them, and in all
+};
+__device__ __forceinline__ Small look_small(const Pool& p) {
+    Small s;
+    const int run = static_cast<int>((p.num_pages + 4 * ONE_THREADS - 1) / (4 * ONE_THREADS) * 4);
+    s.mine = static_cast<long long>(run) * threadIdx.x;
+    s.bits = free_bits<SMALL_POOL / ONE_THREADS>(p, s.mine, p.num_pages, run);
+    s.rank = block_scan<ONE_THREADS>(__popcll(s.bits), &s.total);
+    return s;
 }
 
 }  // namespace pg
@@ -293,25 +324,50 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
     }
 }
 
-// Block c < chunks: free pages of chunk c.  Block `chunks`: the rows that need
-// a fresh page, in order.
+// The rows that need a fresh page, in order: how many.
+template <int T>
+__device__ __forceinline__ int fork_list(const ForkParams& p) {
+    int* list = p.ws.rows + pg::MAX_ROWS;
+    int at = 0;
+    for (int r0 = 0; r0 < p.rows_out; r0 += T) {
+        const int r = r0 + threadIdx.x;
+        const int f = r < p.rows_out ? p.ws.rows[r] : 0;
+        int total;
+        const int k = pg::block_scan<T>(f, &total);
+        if (f) list[at + k] = r;
+        at += total;
+    }
+    return at;
+}
+// The k-th fresh page.
+__device__ __forceinline__ void fork_give(const ForkParams& p, long long id, long long k) {
+    const int r = p.ws.rows[pg::MAX_ROWS + k], par = p.parent[r], page = static_cast<int>(id);
+    const int j = pg::pages_of(p.lens[par], p.shift, p.max_pages) - 1;
+    p.out_table[static_cast<size_t>(r) * p.max_pages + j] = page;
+    p.copy_src[r] = p.table[static_cast<size_t>(par) * p.max_pages + j];
+    p.copy_dst[r] = page;
+    p.pool.refs[page] = 1;
+}
+// The pool is used up after `got` pages: the rows at the end of the list keep
+// their full pages.
+template <int T>
+__device__ __forceinline__ void fork_short(const ForkParams& p, int got, int need, int pool_bit) {
+    for (int k = got + threadIdx.x; k < need; k += T) {
+        const int r = p.ws.rows[pg::MAX_ROWS + k];
+        p.out_lens[r] = p.lens[p.parent[r]] & ~((1 << p.shift) - 1);
+    }
+    if (threadIdx.x == 0) p.ws.head->status = pool_bit;
+}
+
+// Block c < chunks: free pages of chunk c.  Block `chunks`: the list.
 __global__ void __launch_bounds__(pg::THREADS) fork_count_kernel(const ForkParams p) {
     using namespace pg;
     pdl_launch_dependents();
     pdl_wait_primary();
     const int tid = threadIdx.x;
     if (static_cast<int>(blockIdx.x) == p.pool.chunks) {
-        int* list = p.ws.rows + MAX_ROWS;
-        int at = 0;
-        for (int r0 = 0; r0 < p.rows_out; r0 += THREADS) {
-            const int r = r0 + tid;
-            const int f = r < p.rows_out ? p.ws.rows[r] : 0;
-            int total;
-            const int k = block_scan(f, &total);
-            if (f) list[at + k] = r;
-            at += total;
-        }
-        if (tid == 0) p.ws.head->need_list = at;
+        const int n = fork_list<THREADS>(p);
+        if (tid == 0) p.ws.head->need_list = n;
         return;
     }
     const unsigned n = count_chunk(p.pool, blockIdx.x);
@@ -321,28 +377,26 @@ __global__ void __launch_bounds__(pg::THREADS) fork_count_kernel(const ForkParam
 __global__ void __launch_bounds__(pg::THREADS) fork_assign_kernel(const ForkParams p, const int pool_bit) {
     using namespace pg;
     pdl_wait_primary();
-    const int tid = threadIdx.x, chunk = blockIdx.x;
+    const int chunk = blockIdx.x;
     const int need = p.ws.head->need_list;
     if (need == 0) return;
-    const unsigned bits = free_bits(p.pool, chunk * p.pool.chunk + RUN * tid, chunk_end(p.pool, chunk));
-    const int* list = p.ws.rows + MAX_ROWS;
+    const uint64_t bits =
+        free_bits<RUN>(p.pool, chunk * p.pool.chunk + RUN * threadIdx.x, chunk_end(p.pool, chunk), RUN);
     const uint2 f = free_before(p.ws, p.pool.chunks, chunk);
-    if (chunk == 0 && f.y < static_cast<unsigned>(need)) {
-        // the pool is used up: the rows at the end of the list keep their full pages
-        for (int k = static_cast<int>(f.y) + tid; k < need; k += THREADS) {
-            const int r = list[k];
-            p.out_lens[r] = p.lens[p.parent[r]] & ~((1 << p.shift) - 1);
-        }
-        if (tid == 0) atomicOr(&p.ws.head->status, pool_bit);
-    }
-    hand_out(p.pool, chunk, bits, f.x, need, [&](long long id, long long k) {
-        const int r = list[k], par = p.parent[r], page = static_cast<int>(id);
-        const int j = pages_of(p.lens[par], p.shift, p.max_pages) - 1;
-        p.out_table[static_cast<size_t>(r) * p.max_pages + j] = page;
-        p.copy_src[r] = p.table[static_cast<size_t>(par) * p.max_pages + j];
-        p.copy_dst[r] = page;
-        p.pool.refs[page] = 1;
-    });
+    if (chunk == 0 && f.y < static_cast<unsigned>(need)) fork_short<THREADS>(p, f.y, need, pool_bit);
+    hand_out_chunk(p.pool, chunk, bits, f.x, need, [&](long long id, long long k) { fork_give(p, id, k); });
+}
+
+// Both for a small pool.
+__global__ void __launch_bounds__(pg::ONE_THREADS) fork_assign_small_kernel(const ForkParams p, const int pool_bit) {
+    using namespace pg;
+    pdl_wait_primary();
+    const Small s = look_small(p.pool);
+    const int need = fork_list<ONE_THREADS>(p);
+    __syncthreads();   // the list, in global memory, is this block's own
+    if (s.total < need) fork_short<ONE_THREADS>(p, s.total, need, pool_bit);
+    hand_out<ONE_THREADS>(s.bits, s.mine, s.rank, s.total < need ? s.total : need, 0,
+                          [&](long long id, long long k) { fork_give(p, id, k); });
 }
 
 // ---------------------------------------------------------------------------
@@ -357,39 +411,89 @@ struct ExtendParams {
     pg::Ws ws;
 };
 
-// Block c < chunks: free pages of chunk c.  Block `chunks`: each row's length
-// and the pages that the rows before it need.
+// Lengths, and the pages that the rows before each row need: put(r, len,
+// before).  Returns the pages needed in all; *over: a row would outgrow the
+// table.
+template <int T, class F>
+__device__ __forceinline__ int extend_rows(const ExtendParams& p, bool* over, F put) {
+    int at = 0;
+    bool big = false;
+    for (int r0 = 0; r0 < p.rows; r0 += T) {
+        const int r = r0 + threadIdx.x;
+        int need = 0, len = -1;
+        if (r < p.rows) {
+            len = p.lens[r];
+            if (len >= 0) {
+                const long long ps = 1 << p.shift;
+                const long long n_old = (len + ps - 1) >> p.shift;
+                const long long n_new = (static_cast<long long>(len) + p.L + ps - 1) >> p.shift;
+                need = static_cast<int>(n_new - n_old);
+                big |= n_new > p.max_pages;
+            }
+        }
+        int total;
+        const int k = pg::block_scan<T>(need, &total);
+        if (r < p.rows) put(r, len, at + k);
+        at += total;
+    }
+    *over = __syncthreads_or(big) != 0;
+    return at;
+}
+// Positions of the tokens t = first, first + stride ..., and cache rows of
+// those in pages that the row has already (-1: no place).
+template <class Len>
+__device__ __forceinline__ void extend_tokens(const ExtendParams& p, unsigned first, unsigned stride, bool ok, Len lens) {
+    const unsigned tokens = static_cast<unsigned>(p.rows) * p.L, L = p.L;   // at most 2^28
+    const int mask = (1 << p.shift) - 1;
+    for (unsigned t = first; t < tokens; t += stride) {
+        const int r = static_cast<int>(t / L), j = static_cast<int>(t % L);
+        const int len = lens(r);
+        const long long pos = len < 0 ? 0 : static_cast<long long>(len) + j;
+        p.positions[t] = pos;
+        if (len < 0 || !ok) {
+            p.cache_loc[t] = -1;
+        } else if ((pos >> p.shift) < ((static_cast<long long>(len) + mask) >> p.shift)) {
+            const int page = p.table[static_cast<size_t>(r) * p.max_pages + (pos >> p.shift)];
+            p.cache_loc[t] = page < 0 || page >= p.pool.num_pages
+                                 ? -1
+                                 : (static_cast<long long>(page) << p.shift) + (pos & mask);
+        }
+    }
+}
+// The k-th fresh page: its row is the last one with at most k pages needed
+// before it.
+__device__ __forceinline__ void extend_give(const ExtendParams& p, const int* prefix, const int* lens, long long page,
+                                            long long k) {
+    int lo = 0, hi = p.rows - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= k) lo = mid;
+        else hi = mid - 1;
+    }
+    const int mask = (1 << p.shift) - 1;
+    const long long len = lens[lo], slot = ((len + mask) >> p.shift) + (k - prefix[lo]);
+    p.table[static_cast<size_t>(lo) * p.max_pages + slot] = static_cast<int>(page);
+    p.pool.refs[page] = 1;
+    long long j = (slot << p.shift) - len;
+    if (j < 0) j = 0;
+    for (; j < p.L && ((len + j) >> p.shift) == slot; ++j)
+        p.cache_loc[static_cast<long long>(lo) * p.L + j] = (page << p.shift) + ((len + j) & mask);
+}
+
+// Block c < chunks: free pages of chunk c.  Block `chunks`: the rows.
 __global__ void __launch_bounds__(pg::THREADS) extend_count_kernel(const ExtendParams p) {
     using namespace pg;
     pdl_launch_dependents();
     const int tid = threadIdx.x;
     if (static_cast<int>(blockIdx.x) == p.pool.chunks) {
-        int at = 0;
-        bool over = false;
-        for (int r0 = 0; r0 < p.rows; r0 += THREADS) {
-            const int r = r0 + tid;
-            int need = 0;
-            if (r < p.rows) {
-                const int len = p.lens[r];
-                p.ws.rows[r] = len;
-                if (len >= 0) {
-                    const long long ps = 1 << p.shift;
-                    const long long n_old = (len + ps - 1) >> p.shift;
-                    const long long n_new = (static_cast<long long>(len) + p.L + ps - 1) >> p.shift;
-                    need = static_cast<int>(n_new - n_old);
-                    over |= n_new > p.max_pages;
-                }
-            }
-            int total;
-            const int k = block_scan(need, &total);
-            if (r < p.rows) p.ws.prefix[r] = at + k;
-            at += total;
-        }
-        const int any = __syncthreads_or(over);
+        bool over;
+        const int need = extend_rows<THREADS>(p, &over, [&](int r, int len, int before) {
+            p.ws.rows[r] = len;
+            p.ws.prefix[r] = before;
+        });
         if (tid == 0) {
-            p.ws.prefix[p.rows] = at;
-            p.ws.head->need = at;
-            p.ws.head->row_overflow = any;
+            p.ws.head->need = need;
+            p.ws.head->row_overflow = over;
         }
         return;
     }
@@ -405,8 +509,8 @@ __global__ void __launch_bounds__(pg::THREADS)
     const bool pool_block = chunk < p.pool.chunks;
     // The counts change in this kernel only, a chunk by its own block.  Pages are
     // usually found in the first chunks, which look early.
-    unsigned bits = 0;
-    auto look = [&] { bits = free_bits(p.pool, chunk * p.pool.chunk + RUN * tid, chunk_end(p.pool, chunk)); };
+    uint64_t bits = 0;
+    auto look = [&] { bits = free_bits<RUN>(p.pool, chunk * p.pool.chunk + RUN * tid, chunk_end(p.pool, chunk), RUN); };
     if (pool_block && chunk < EARLY_CHUNKS) look();
     pdl_wait_primary();
     const int need = p.ws.head->need;
@@ -414,24 +518,7 @@ __global__ void __launch_bounds__(pg::THREADS)
     const uint2 f = free_before(p.ws, p.pool.chunks, chunk);
     const bool enough = static_cast<unsigned>(need) <= f.y, ok = !over && enough;
     if (chunk == 0 && tid == 0) p.ws.head->status = (over ? row_bit : 0) | (enough ? 0 : pool_bit);
-
-    // tokens in pages that the row has already (and those that get no place)
-    const unsigned tokens = static_cast<unsigned>(p.rows) * p.L, L = p.L;   // at most 2^28
-    const int mask = (1 << p.shift) - 1;
-    for (unsigned t = blockIdx.x * THREADS + tid; t < tokens; t += gridDim.x * THREADS) {
-        const int r = static_cast<int>(t / L), j = static_cast<int>(t % L);
-        const int len = p.ws.rows[r];
-        const long long pos = len < 0 ? 0 : static_cast<long long>(len) + j;
-        p.positions[t] = pos;
-        if (len < 0 || !ok) {
-            p.cache_loc[t] = -1;
-        } else if ((pos >> p.shift) < ((static_cast<long long>(len) + mask) >> p.shift)) {
-            const int page = p.table[static_cast<size_t>(r) * p.max_pages + (pos >> p.shift)];
-            p.cache_loc[t] = page < 0 || page >= p.pool.num_pages
-                                 ? -1
-                                 : (static_cast<long long>(page) << p.shift) + (pos & mask);
-        }
-    }
+    extend_tokens(p, blockIdx.x * THREADS + tid, gridDim.x * THREADS, ok, [&](int r) { return p.ws.rows[r]; });
     if (!ok) return;
     if (chunk == 0)
         for (int r = tid; r < p.rows; r += THREADS)
@@ -444,22 +531,29 @@ __global__ void __launch_bounds__(pg::THREADS)
         s_prefix[r] = p.ws.prefix[r];
         s_len[r] = p.ws.rows[r];
     }
-    __syncthreads();
-    hand_out(p.pool, chunk, bits, f.x, need, [&](long long page, long long k) {
-        int lo = 0, hi = p.rows - 1;   // the last row whose prefix is at most k
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_prefix[mid] <= k) lo = mid;
-            else hi = mid - 1;
-        }
-        const long long len = s_len[lo], slot = ((len + mask) >> p.shift) + (k - s_prefix[lo]);
-        p.table[static_cast<size_t>(lo) * p.max_pages + slot] = static_cast<int>(page);
-        p.pool.refs[page] = 1;
-        long long j = (slot << p.shift) - len;
-        if (j < 0) j = 0;
-        for (; j < p.L && ((len + j) >> p.shift) == slot; ++j)
-            p.cache_loc[static_cast<long long>(lo) * p.L + j] = (page << p.shift) + ((len + j) & mask);
-    });
+    hand_out_chunk(p.pool, chunk, bits, f.x, need,
+                   [&](long long page, long long k) { extend_give(p, s_prefix, s_len, page, k); });
+}
+
+// Both for a small pool.
+__global__ void __launch_bounds__(pg::ONE_THREADS)
+    extend_small_kernel(const ExtendParams p, const int pool_bit, const int row_bit) {
+    using namespace pg;
+    __shared__ int s_prefix[MAX_ROWS], s_len[MAX_ROWS];
+    const Small s = look_small(p.pool);
+    bool over;
+    const int need = extend_rows<ONE_THREADS>(p, &over, [&](int r, int len, int before) {
+        s_len[r] = len;
+        s_prefix[r] = before;
+    });   // its last barrier covers the tables
+    const bool enough = need <= s.total, ok = !over && enough;
+    if (threadIdx.x == 0) p.ws.head->status = (over ? row_bit : 0) | (enough ? 0 : pool_bit);
+    extend_tokens(p, threadIdx.x, ONE_THREADS, ok, [&](int r) { return s_len[r]; });
+    if (!ok) return;
+    for (int r = threadIdx.x; r < p.rows; r += ONE_THREADS)
+        if (s_len[r] >= 0) p.lens[r] = s_len[r] + p.L;
+    hand_out<ONE_THREADS>(s.bits, s.mine, s.rank, need, 0,
+                          [&](long long page, long long k) { extend_give(p, s_prefix, s_len, page, k); });
 }
 
 // ---------------------------------------------------------------------------
@@ -518,56 +612,100 @@ __global__ void __launch_bounds__(pg::THREADS) compact_count_kernel(const Compac
 
 // With `total` pages in use, the k-th page in use at or above `total` moves to
 // the k-th free page below it: sources and destinations are two disjoint
-// ranges of the pool, and no page moves that need not.
+// ranges of the pool, and no page moves that need not.  `holes`: free pages
+// below `total`, as many as pages that would move.
+struct Moves {
+    long long total, kept;   // pages in use; those of them below `total`
+    int moves;
+};
+__device__ __forceinline__ Moves compact_moves(const CompactParams& p, long long total, long long holes) {
+    return {total, total - holes, static_cast<int>(holes < p.max_moves ? holes : p.max_moves)};
+}
+// For the first thread of the first block: what the next kernel and the caller get.
+__device__ __forceinline__ void compact_head(const CompactParams& p, const Moves& m) {
+    p.used[0] = static_cast<int>(m.total);
+    p.ws.head->total = static_cast<int>(m.total);
+    p.ws.head->moves = m.moves;
+    p.ws.head->status = 0;
+}
+// Pages id, k free ones before it.
+__device__ __forceinline__ void compact_page(const CompactParams& p, const Moves& m, long long id, long long k, bool free) {
+    if (free) {
+        if (id < m.total && k < m.moves) p.copy_dst[k] = static_cast<int>(id);
+        if (id >= m.total) p.ws.rank[id] = -1;
+    } else if (id >= m.total) {
+        const long long q = id - k - m.kept;   // id - k pages in use come before this one
+        if (q < m.moves) p.copy_src[q] = static_cast<int>(id);
+        p.ws.rank[id] = q < m.moves ? static_cast<int>(q) : -1;
+    }
+}
+
 __global__ void __launch_bounds__(pg::THREADS) compact_rank_kernel(const CompactParams p) {
     using namespace pg;
+    __shared__ uint16_t s_bits[THREADS];
+    __shared__ int s_rank[THREADS];
     const int tid = threadIdx.x, chunk = blockIdx.x;
     const long long i0 = chunk * p.pool.chunk, i1 = chunk_end(p.pool, chunk);
-    unsigned bits = free_bits(p.pool, i0 + RUN * tid, i1);   // the counts change in the next kernel only
+    uint64_t bits = free_bits<RUN>(p.pool, i0 + RUN * tid, i1, RUN);   // the counts change in the next kernel only
     pdl_launch_dependents();
     pdl_wait_primary();
     const uint2 f = free_before(p.ws, p.pool.chunks, chunk);
     const long long total = p.pool.num_pages - f.y;
-    // holes: free pages below `total`, as many as pages that would move; the
-    // chunk that `total` lies in is counted up to it
+    // the chunk that `total` lies in is counted up to it
     const int edge = static_cast<int>(total / p.pool.chunk);
     unsigned whole = 0, part = 0;
     for (int i = tid; i < edge; i += THREADS) whole += p.ws.counts[i];
     for (long long i = edge * p.pool.chunk + tid; i < total; i += THREADS) part += p.pool.refs[i] == 0;
-    const uint2 h = block_sum2(whole, part);
-    const long long holes = static_cast<long long>(h.x) + h.y, kept = total - holes;
-    const int moves = static_cast<int>(holes < p.max_moves ? holes : p.max_moves);
-    if (chunk == 0 && tid == 0) {
-        p.used[0] = static_cast<int>(total);
-        p.ws.head->total = static_cast<int>(total);
-        p.ws.head->moves = moves;
-        p.ws.head->status = 0;
-    }
-    for (long long k = moves + static_cast<long long>(chunk) * THREADS + tid; k < p.max_moves;
+    const uint2 h = block_sum2<THREADS>(whole, part);
+    const Moves m = compact_moves(p, total, static_cast<long long>(h.x) + h.y);
+    if (chunk == 0 && tid == 0) compact_head(p, m);
+    for (long long k = m.moves + static_cast<long long>(chunk) * THREADS + tid; k < p.max_moves;
          k += static_cast<long long>(gridDim.x) * THREADS) {
         p.copy_src[k] = -1;
         p.copy_dst[k] = -1;
     }
     long long before = f.x;   // free pages before the next ones
     for (long long i = i0; i < i1; i += CHUNK) {
-        const long long mine = i + RUN * tid;
-        if (i != i0) bits = free_bits(p.pool, mine, i1);
+        if (i != i0) bits = free_bits<RUN>(p.pool, i + RUN * tid, i1, RUN);
         int sum;
-        long long k = before + block_scan(__popc(bits), &sum);
-#pragma unroll
-        for (int u = 0; u < RUN; ++u) {
-            const long long id = mine + u;
-            if (bits >> u & 1) {
-                if (id < total && k < moves) p.copy_dst[k] = static_cast<int>(id);
-                if (id >= total) p.ws.rank[id] = -1;
-                ++k;
-            } else if (id < i1 && id >= total) {
-                const long long m = id - k - kept;   // id - k pages in use come before this one
-                if (m < moves) p.copy_src[m] = static_cast<int>(id);
-                p.ws.rank[id] = m < moves ? static_cast<int>(m) : -1;
-            }
+        const int rank = block_scan<THREADS>(__popcll(bits), &sum);
+        // neighbouring threads write neighbouring places: page by page, not run by run
+        s_bits[tid] = static_cast<uint16_t>(bits);
+        s_rank[tid] = rank;
+        __syncthreads();
+#pragma unroll 4
+        for (int o = tid; o < CHUNK; o += THREADS) {
+            const unsigned b = s_bits[o / RUN], at = o % RUN;
+            if (i + o < i1)
+                compact_page(p, m, i + o, before + s_rank[o / RUN] + __popc(b & ((1u << at) - 1)), b >> at & 1);
         }
         before += sum;
+    }
+}
+static_assert(pg::RUN <= 16, "a run's bits");
+
+// Both for a small pool.
+__global__ void __launch_bounds__(pg::ONE_THREADS) compact_small_kernel(const CompactParams p) {
+    using namespace pg;
+    __shared__ uint64_t s_bits[ONE_THREADS];
+    __shared__ int s_rank[ONE_THREADS];
+    const int tid = threadIdx.x;
+    pdl_launch_dependents();
+    const Small s = look_small(p.pool);
+    const long long total = p.pool.num_pages - s.total;
+    const long long below = total - s.mine;   // the thread's pages below `total`
+    const uint64_t low = below >= 64 ? s.bits : below > 0 ? s.bits & ((1ull << below) - 1) : 0;
+    const Moves m = compact_moves(p, total, block_sum2<ONE_THREADS>(__popcll(low), 0).x);
+    if (tid == 0) compact_head(p, m);
+    for (int k = m.moves + tid; k < p.max_moves; k += ONE_THREADS) p.copy_src[k] = p.copy_dst[k] = -1;
+    s_bits[tid] = s.bits;
+    s_rank[tid] = s.rank;
+    __syncthreads();
+    const int run = static_cast<int>((p.pool.num_pages + 4 * ONE_THREADS - 1) / (4 * ONE_THREADS) * 4);
+    for (int id = tid; id < p.pool.num_pages; id += ONE_THREADS) {
+        const int who = id / run, at = id - who * run;
+        const uint64_t b = s_bits[who];
+        compact_page(p, m, id, s_rank[who] + __popcll(b & ((1ull << at) - 1)), b >> at & 1);
     }
 }
 

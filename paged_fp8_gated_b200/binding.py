@@ -626,9 +626,10 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, K: int, finished: to
         out = _make(stream, lambda: tuple(torch.empty(G, K, dtype=dt, device=dev)
                                           for dt in (torch.float32, torch.int32, torch.int32)))
     else:
-        for t, n, dt in zip(out, ("out scores", "out parent", "out token"),
-                            (torch.float32, torch.int32, torch.int32), strict=True):
-            _cuda(t, n, dev, dt, (G, K))
+        best, parent, token = out
+        _cuda(best, "out scores", dev, torch.float32, (G, K))
+        _cuda(parent, "out parent", dev, torch.int32, (G, K))
+        _cuda(token, "out token", dev, torch.int32, (G, K))
     if workspace is None:
         workspace = _make(stream, lambda: alloc_beam_workspace(G, W, V, K, dev))
     else:
@@ -670,6 +671,9 @@ def _pages_ws(workspace, rows, num_pages, dev, stream):
     return _cuda(workspace, "workspace", dev, torch.uint8)
 
 
+_CACHE_DTYPES = (torch.uint8, torch.float8_e4m3fn)
+
+
 def pages_copy(caches: list[torch.Tensor], src: torch.Tensor, dst: torch.Tensor,
                stream: torch.cuda.Stream | None = None) -> None:
     """Copies page src[i] to page dst[i] in every cache of the list (uint8 or E4M3
@@ -681,11 +685,14 @@ def pages_copy(caches: list[torch.Tensor], src: torch.Tensor, dst: torch.Tensor,
     if not caches:
         raise ValueError("caches must hold at least one tensor")
     shape = caches[0].shape
-    for i, c in enumerate(caches):
-        _cuda(c, f"caches[{i}]", dev, torch.uint8 if c.dtype != torch.float8_e4m3fn else c.dtype, shape)
+    ptrs = []
+    for c in caches:
+        if not (c.shape == shape and c.dtype in _CACHE_DTYPES and c.is_contiguous() and c.device == dev):
+            _cuda(c, f"caches[{len(ptrs)}]", dev, torch.uint8, shape)
+        ptrs.append(c.data_ptr())
     num_pages = shape[0] if shape else 0
     page_bytes = caches[0].numel() // num_pages if num_pages else 0
-    ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+    ptrs = (ctypes.c_void_p * len(ptrs))(*ptrs)
     _call(_lib.gad_pages_copy, dev, stream, ptrs, len(caches), page_bytes, num_pages, src.data_ptr(),
           dst.data_ptr(), n)
 
@@ -704,9 +711,11 @@ def pages_fork(page_table: torch.Tensor, lens: torch.Tensor, parent: torch.Tenso
         out = _make(stream, lambda: (torch.full((n, max_pages), -1, dtype=torch.int32, device=dev),
                                      *(torch.empty(n, dtype=torch.int32, device=dev) for _ in range(3))))
     else:
-        for t, name, shape in zip(out, ("out table", "out lens", "copy_src", "copy_dst"),
-                                  ((n, max_pages), (n,), (n,), (n,)), strict=True):
-            _cuda(t, name, dev, torch.int32, shape)
+        table, new_lens, src, dst = out
+        _cuda(table, "out table", dev, torch.int32, (n, max_pages))
+        _cuda(new_lens, "out lens", dev, torch.int32, (n,))
+        _cuda(src, "copy_src", dev, torch.int32, (n,))
+        _cuda(dst, "copy_dst", dev, torch.int32, (n,))
     ws = _pages_ws(workspace, max(rows, n), num_pages, dev, stream)
     _call(_lib.gad_pages_fork, dev, stream, page_table.data_ptr(), lens.data_ptr(), rows, parent.data_ptr(),
           n, max_pages, int(page_size), refs.data_ptr(), num_pages, *(t.data_ptr() for t in out),
@@ -725,8 +734,9 @@ def pages_extend(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tenso
         out = _make(stream, lambda: tuple(torch.empty(rows * max(int(L), 0), dtype=torch.int64, device=dev)
                                           for _ in range(2)))
     else:
-        for t, name in zip(out, ("positions", "cache_loc"), strict=True):
-            _cuda(t, name, dev, torch.int64, (rows * L,))
+        positions, cache_loc = out
+        _cuda(positions, "positions", dev, torch.int64, (rows * L,))
+        _cuda(cache_loc, "cache_loc", dev, torch.int64, (rows * L,))
     ws = _pages_ws(workspace, rows, num_pages, dev, stream)
     _call(_lib.gad_pages_extend, dev, stream, page_table.data_ptr(), lens.data_ptr(), rows, int(L),
           max_pages, int(page_size), refs.data_ptr(), num_pages, out[0].data_ptr(), out[1].data_ptr(),
@@ -758,8 +768,10 @@ def pages_compact(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tens
                                           for n in (m, m, 1)))
     else:
         m = out[0].numel() if max_moves is None else int(max_moves)
-        for t, name, shape in zip(out, ("copy_src", "copy_dst", "used"), ((m,), (m,), (1,)), strict=True):
-            _cuda(t, name, dev, torch.int32, shape)
+        src, dst, used = out
+        _cuda(src, "copy_src", dev, torch.int32, (m,))
+        _cuda(dst, "copy_dst", dev, torch.int32, (m,))
+        _cuda(used, "used", dev, torch.int32, (1,))
     ws = _pages_ws(workspace, rows, num_pages, dev, stream)
     _call(_lib.gad_pages_compact, dev, stream, page_table.data_ptr(), lens.data_ptr(), rows, max_pages,
           int(page_size), refs.data_ptr(), num_pages, out[0].data_ptr(), out[1].data_ptr(), m,

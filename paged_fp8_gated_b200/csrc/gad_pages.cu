@@ -101,10 +101,12 @@ int launch(const char* name, void (*kern)(Params...), dim3 grid, int threads, cu
 }
 
 constexpr int T = gad::pg::THREADS;
-// Most tokens that extend's one block for a small pool places.
-constexpr long long kSmallTokens = 16384;
+// Blocks of four columns a thread below which fork takes one: 148 SMs.
+constexpr long long kFewBlocks = 148;
+// Most tokens that extend's cluster for a small pool places.
+constexpr long long kSmallTokens = 65536;
 
-// Whether a kernel of one block looks through the pool.
+// Whether a kernel of one cluster looks through the pool.
 bool small_pool(int64_t num_pages) { return num_pages <= gad::pg::SMALL_POOL; }
 
 int shift_of(int page_size) { return page_size == 64 ? 6 : 0; }
@@ -208,13 +210,19 @@ int gad_pages_fork(const int32_t* page_table, const int32_t* lens, int rows_in, 
     p.pool = bind_pool(refs, num_pages);
     p.ws = bind_ws(workspace, num_pages);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int rows = rows_in > rows_out ? rows_in : rows_out;
+    const bool few = static_cast<long long>(blocks(rows, gad::pg::ROWS)) * blocks(max_pages, 4 * T) < kFewBlocks;
     const bool vec = max_pages % 4 == 0 && aligned(page_table, 16) && aligned(out_table, 16);
-    const dim3 grid(blocks(max_pages, gad::pg::COLS), blocks(rows_in > rows_out ? rows_in : rows_out, gad::pg::ROWS));
-    st = launch("fork", vec ? gad::fork_kernel<true> : gad::fork_kernel<false>, grid, T, s, false, p);
+    const dim3 grid(blocks(max_pages, few ? T : 4 * T), blocks(rows, gad::pg::ROWS));
+    st = launch("fork",
+                few   ? gad::fork_kernel<1, false>
+                : vec ? gad::fork_kernel<4, true>
+                      : gad::fork_kernel<4, false>,
+                grid, T, s, false, p);
     if (st != GAD_OK || page_size == 1) return st;   // single-token pages are never partly filled
     const int pool_bit = GAD_STATUS_PAGES_POOL;
     if (small_pool(num_pages))
-        return launch("fork assign", gad::fork_assign_small_kernel, dim3(1), gad::pg::ONE_THREADS, s, true, p, pool_bit);
+        return launch("fork assign", gad::fork_assign_small_kernel, dim3(gad::pg::SMALL_BLOCKS), gad::pg::SMALL_THREADS, s, true, p, pool_bit);
     st = launch("fork count", gad::fork_count_kernel, dim3(p.pool.chunks + 1), T, s, true, p);
     if (st != GAD_OK) return st;
     return launch("fork assign", gad::fork_assign_kernel, dim3(p.pool.chunks), T, s, true, p, pool_bit);
@@ -252,7 +260,7 @@ int gad_pages_extend(int32_t* page_table, int32_t* lens, int rows, int L, int ma
     const int pool_bit = GAD_STATUS_PAGES_POOL, row_bit = GAD_STATUS_PAGES_ROW;
     const long long tokens = static_cast<long long>(rows) * L;
     if (small_pool(num_pages) && tokens <= kSmallTokens)
-        return launch("extend", gad::extend_small_kernel, dim3(1), gad::pg::ONE_THREADS, s, false, p, pool_bit, row_bit);
+        return launch("extend", gad::extend_small_kernel, dim3(gad::pg::SMALL_BLOCKS), gad::pg::SMALL_THREADS, s, false, p, pool_bit, row_bit);
     st = launch("extend count", gad::extend_count_kernel, dim3(p.pool.chunks + 1), T, s, false, p);
     if (st != GAD_OK) return st;
     // enough blocks for the tokens' rows too
@@ -283,12 +291,21 @@ int gad_pages_free(const int32_t* page_table, int32_t* lens, int rows, const uin
     p.shift = shift_of(page_size);
     p.refs = refs;
     p.num_pages = num_pages;
-    // four entries a thread: blocks of up to 1024 threads, up to eight of them
-    // (the portable cluster size) per row
+    // four entries a thread: blocks of up to 1024 threads, up to sixteen of them
+    // per row (more than eight is a size that a kernel has to allow)
     int threads = 64;
     while (threads < 1024 && threads * 4 < max_pages) threads *= 2;
     p.parts = 1;
-    while (p.parts < 8 && static_cast<long long>(p.parts) * threads * 4 < max_pages) p.parts *= 2;
+    while (p.parts < 16 && static_cast<long long>(p.parts) * threads * 4 < max_pages) p.parts *= 2;
+    static OncePerContext allowed;
+    int dev = 0;
+    st = current_device(&dev);
+    if (st != GAD_OK) return st;
+    if (!allowed.is_done(dev, current_ctx_id())) {
+        const cudaError_t e = cudaFuncSetAttribute(gad::free_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        allowed.mark(dev);
+    }
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * p.parts);
@@ -338,16 +355,15 @@ int gad_pages_compact(int32_t* page_table, const int32_t* lens, int rows, int ma
     p.ws = bind_ws(workspace, num_pages);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (small_pool(num_pages)) {
-        st = launch("compact", gad::compact_small_kernel, dim3(1), gad::pg::ONE_THREADS, s, false, p);
+        st = launch("compact", gad::compact_small_kernel, dim3(gad::pg::SMALL_BLOCKS), gad::pg::SMALL_THREADS, s, false, p);
     } else {
         st = launch("compact count", gad::compact_count_kernel, dim3(p.pool.chunks), T, s, false, p);
         if (st != GAD_OK) return st;
         st = launch("compact rank", gad::compact_rank_kernel, dim3(p.pool.chunks), T, s, true, p);
     }
     if (st != GAD_OK) return st;
-    const unsigned gx = blocks(max_pages, 4 * T);
-    return launch("compact apply", gad::compact_apply_kernel,
-                  dim3(gx < 1024 ? gx : 1024, static_cast<unsigned>(rows) + 1), T, s, true, p);
+    const unsigned gx = blocks(max_pages, 4 * T);   // four entries a thread
+    return launch("compact apply", gad::compact_apply_kernel, dim3(gx < 1024 ? gx : 1024, static_cast<unsigned>(rows) + 1), T, s, true, p);
 }
 
 }  // extern "C"

@@ -14,8 +14,9 @@
 // the free pages per chunk of the pool, a second one ranks the free pages of
 // each chunk behind the sum of the chunks before it and gives each to its row.
 // Both read the counts once (4 bytes a page).  A pool of at most SMALL_POOL pages
-// is looked at by one block, which keeps the free pages as bits between the two
-// and saves a launch.  Page ids outside [0, num_pages) are skipped everywhere.
+// is looked at by one cluster, which keeps the free pages as bits between the
+// two and saves a launch.  Page ids outside [0, num_pages) are skipped
+// everywhere.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -30,12 +31,11 @@ constexpr int THREADS = 256;
 constexpr int CHUNK = 4096;          // pages per chunk, unless the pool has more than MAX_CHUNKS of them
 constexpr int MAX_CHUNKS = 1024;
 constexpr int MAX_ROWS = 4096;
-constexpr int COLS = 4 * THREADS;    // fork: table columns per block, four a thread
 constexpr int ROWS = 8;              // fork: table rows per block
 constexpr int RUN = CHUNK / THREADS; // pages of a chunk that a thread looks at
 constexpr int EARLY_CHUNKS = 16;     // chunks that extend looks at before it knows that it must
-constexpr int ONE_THREADS = 1024;    // threads of a kernel of one block
-constexpr int SMALL_POOL = 64 * ONE_THREADS;
+constexpr int SMALL_BLOCKS = 8, SMALL_THREADS = 512;   // the cluster for a small pool
+constexpr int SMALL_POOL = SMALL_BLOCKS * SMALL_THREADS * 16;
 constexpr int LIST = 2048;           // free pages that are handed out at a time
 constexpr int MAX_CACHES = 64;       // caches per copy launch
 
@@ -125,15 +125,13 @@ __device__ __forceinline__ int4 refs4(const Pool& p, long long i, int past) {
     return r;
 }
 
-// Which of the `run` pages from i on are free, as bits (i and run multiples of
-// 4, run at most MAX_RUN).
-template <int MAX_RUN>
-__device__ __forceinline__ uint64_t free_bits(const Pool& p, long long i, long long end, int run) {
-    uint64_t bits = 0;
+// Which of the RUN pages from i on are free, as bits (i a multiple of 4).
+__device__ __forceinline__ unsigned free_bits(const Pool& p, long long i, long long end) {
+    unsigned bits = 0;
 #pragma unroll
-    for (int u = 0; u < MAX_RUN; u += 4) {
-        const int4 r = u < run && i + u < end ? refs4(p, i + u, 1) : make_int4(1, 1, 1, 1);
-        bits |= static_cast<uint64_t>((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << u;
+    for (int u = 0; u < RUN; u += 4) {
+        const int4 r = i + u < end ? refs4(p, i + u, 1) : make_int4(1, 1, 1, 1);
+        bits |= static_cast<unsigned>((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << u;
     }
     return bits;
 }
@@ -146,7 +144,7 @@ __device__ __forceinline__ unsigned count_chunk(const Pool& p, int chunk) {
     const long long end = chunk_end(p, chunk);
     unsigned n = 0;
     for (long long i = chunk * p.chunk + RUN * threadIdx.x; i < end; i += CHUNK)
-        n += __popcll(free_bits<RUN>(p, i, end, RUN));
+        n += __popc(free_bits(p, i, end));
     return block_sum2<THREADS>(n, 0).x;
 }
 // Free pages in the chunks before `chunk` (x), and in all of them (y).
@@ -165,13 +163,13 @@ __device__ __forceinline__ uint2 free_before(const Ws& ws, int chunks, int chunk
 // `rank` of the stretch's come before them.  The pages go through shared memory
 // so that all threads give (a give is a chain of loads).
 template <int T, class F>
-__device__ __forceinline__ void hand_out(uint64_t bits, long long mine, int rank, int n, long long before, F give) {
+__device__ __forceinline__ void hand_out(unsigned bits, long long mine, int rank, int n, long long before, F give) {
     __shared__ int s_list[LIST];
     for (int lo = 0; lo < n; lo += LIST) {
         __syncthreads();
         int q = rank - lo;
-        for (uint64_t b = bits; b != 0 && q < LIST; ++q, b &= b - 1)
-            if (q >= 0) s_list[q] = static_cast<int>(mine + __ffsll(b) - 1);
+        for (unsigned b = bits; b != 0 && q < LIST; ++q, b &= b - 1)
+            if (q >= 0) s_list[q] = static_cast<int>(mine + __ffs(b) - 1);
         __syncthreads();
         const int m = n - lo < LIST ? n - lo : LIST;
         for (int i = threadIdx.x; i < m; i += T) give(static_cast<long long>(s_list[i]), before + lo + i);
@@ -180,31 +178,45 @@ __device__ __forceinline__ void hand_out(uint64_t bits, long long mine, int rank
 // The same for a chunk, `before` free pages in the chunks before it, ranks below
 // `need`; `bits`: those of its first CHUNK pages.
 template <class F>
-__device__ __forceinline__ void hand_out_chunk(const Pool& p, int chunk, uint64_t bits, long long before, long long need,
+__device__ __forceinline__ void hand_out_chunk(const Pool& p, int chunk, unsigned bits, long long before, long long need,
                                                F give) {
     const long long end = chunk_end(p, chunk);
     for (long long i0 = chunk * p.chunk; i0 < end && before < need; i0 += CHUNK) {
         const long long mine = i0 + RUN * threadIdx.x;
-        if (i0 != chunk * p.chunk) bits = mine < end ? free_bits<RUN>(p, mine, end, RUN) : 0;
+        if (i0 != chunk * p.chunk) bits = mine < end ? free_bits(p, mine, end) : 0;
         int sum;
-        const int rank = block_scan<THREADS>(__popcll(bits), &sum);
+        const int rank = block_scan<THREADS>(__popc(bits), &sum);
         hand_out<THREADS>(bits, mine, rank, static_cast<int>(sum < need - before ? sum : need - before), before, give);
         before += sum;
     }
 }
-// A pool of at most SMALL_POOL pages as one block sees it.
+// A pool of at most SMALL_POOL pages as a cluster's threads see it.
 struct Small {
-    uint64_t bits;     // the thread's free pages from page `mine` on
-    long long mine;
-    int rank, total;   // free pages before them, and in all
+    unsigned bits;      // the thread's free pages from page `mine` on
+    int mine;
+    int rank, sum;      // free pages before them in the block, and in the block
 };
-__device__ __forceinline__ Small look_small(const Pool& p) {
+__device__ __forceinline__ Small look_small(const Pool& p, int block) {
     Small s;
-    const int run = static_cast<int>((p.num_pages + 4 * ONE_THREADS - 1) / (4 * ONE_THREADS) * 4);
-    s.mine = static_cast<long long>(run) * threadIdx.x;
-    s.bits = free_bits<SMALL_POOL / ONE_THREADS>(p, s.mine, p.num_pages, run);
-    s.rank = block_scan<ONE_THREADS>(__popcll(s.bits), &s.total);
+    s.mine = (block * SMALL_THREADS + static_cast<int>(threadIdx.x)) * RUN;
+    s.bits = free_bits(p, s.mine, p.num_pages);
+    s.rank = block_scan<SMALL_THREADS>(__popc(s.bits), &s.sum);
     return s;
+}
+// What every block of the cluster has in `mine`, added up: over the blocks
+// before this one (x), over all of them (y).  The cluster's threads pass two
+// barriers here.
+__device__ __forceinline__ uint2 cluster_sum(unsigned mine, int block) {
+    __shared__ unsigned s_sum;
+    const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    if (threadIdx.x == 0) s_sum = mine;
+    cluster.sync();
+    const int lane = threadIdx.x & 31;
+    const unsigned v = lane < SMALL_BLOCKS ? *cluster.map_shared_rank(&s_sum, lane) : 0;
+    const uint2 r = make_uint2(__reduce_add_sync(0xffffffffu, lane < block ? v : 0),
+                               __reduce_add_sync(0xffffffffu, v));
+    cluster.sync();   // everyone has read it: it may change, and the block may end
+    return r;
 }
 
 }  // namespace pg
@@ -221,17 +233,20 @@ struct ForkParams {
     pg::Ws ws;
 };
 
-// One block per (COLS columns, ROWS rows).  An old row's pages change their
+// One block per (U THREADS columns, ROWS rows).  An old row's pages change their
 // counts by its children - 1 (of a partly filled last page only the first child
 // takes the page, so its count only falls when there is none); a new row takes
 // its parent's entries.  The entry of a fresh last page is left to
 // fork_assign_kernel.  Rows that share pages are usually neighbours (the beams
 // of a request): a thread adds up what its rows change about the page that they
 // have in common in a column, and a count is touched only if something is left.
-template <bool VEC>
+// Tables that leave the GPU with few blocks take one column a thread (U = 1),
+// larger ones four, as vectors if the rows allow it (VEC).
+template <int U, bool VEC>
 __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
     using namespace pg;
     __shared__ int s_kids[ROWS], s_elder[ROWS], s_par[ROWS], s_len[ROWS], s_new[ROWS];
+    static_assert(!VEC || U == 4, "a vector is four entries");
     const int y0 = blockIdx.y * ROWS, tid = threadIdx.x;
     pdl_launch_dependents();
     if (tid < ROWS) {
@@ -253,25 +268,27 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
     }
     __syncthreads();
 
-    const int c0 = blockIdx.x * COLS;
-    auto col = [&](int u) { return VEC ? c0 + 4 * tid + u : c0 + u * THREADS + tid; };
+    const int c0 = blockIdx.x * (U * THREADS);
+    auto col = [&](int u) { return VEC ? c0 + U * tid + u : c0 + u * THREADS + tid; };
     // the four entries of a row (any value from `n` on)
-    auto entries = [&](int (&e)[4], const int* row, int n) {
+    auto entries = [&](int (&e)[U], const int* row, int n) {
         if (VEC) {
             const int4 q = col(0) < n ? *reinterpret_cast<const int4*>(row + col(0)) : make_int4(-1, -1, -1, -1);
-            e[0] = q.x; e[1] = q.y; e[2] = q.z; e[3] = q.w;
+            e[0] = q.x; e[1 % U] = q.y; e[2 % U] = q.z; e[3 % U] = q.w;
         } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) e[u] = col(u) < n ? row[col(u)] : -1;
+            for (int u = 0; u < U; ++u) e[u] = col(u) < n ? row[col(u)] : -1;
         }
     };
-    int e[ROWS][4];   // all rows' entries at a time
+    int e[ROWS][U];   // all rows' entries at a time
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
         const int n = s_kids[k] == 1 ? 0 : pages_of(s_len[k], p.shift, p.max_pages);
         entries(e[k], p.table + static_cast<size_t>(y0 + k) * p.max_pages, n);
     }
-    int page[4] = {-1, -1, -1, -1}, left[4] = {0, 0, 0, 0};
+    int page[U], left[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) page[u] = -1, left[u] = 0;
     auto flush = [&](int u) {
         if (left[u] != 0 && page[u] >= 0 && page[u] < p.pool.num_pages) atomicAdd(p.pool.refs + page[u], left[u]);
     };
@@ -281,7 +298,7 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
         const int n = kids == 1 ? 0 : pages_of(len, p.shift, p.max_pages);
         const int last = has_partial(len, p.shift, p.max_pages) ? n - 1 : -1;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < U; ++u) {
             if (col(u) >= n) continue;
             const int d = (col(u) == last ? min(kids, 1) : kids) - 1;
             if (e[k][u] != page[u]) {
@@ -293,7 +310,7 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
         }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) flush(u);
+    for (int u = 0; u < U; ++u) flush(u);
 
     auto taken = [&](int k) {   // entries that new row y0 + k takes over
         const bool fresh = s_elder[k] && has_partial(s_new[k], p.shift, p.max_pages);
@@ -307,10 +324,10 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
         const int y = y0 + k, n = taken(k);
         int* dst = p.out_table + static_cast<size_t>(y) * p.max_pages;
         if (VEC && col(3) < n) {
-            *reinterpret_cast<int4*>(dst + col(0)) = make_int4(e[k][0], e[k][1], e[k][2], e[k][3]);
+            *reinterpret_cast<int4*>(dst + col(0)) = make_int4(e[k][0], e[k][1 % U], e[k][2 % U], e[k][3 % U]);
         } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < U; ++u)
                 if (col(u) < n) dst[col(u)] = e[k][u];
         }
     }
@@ -326,8 +343,7 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
 
 // The rows that need a fresh page, in order: how many.
 template <int T>
-__device__ __forceinline__ int fork_list(const ForkParams& p) {
-    int* list = p.ws.rows + pg::MAX_ROWS;
+__device__ __forceinline__ int fork_list(const ForkParams& p, int* list) {
     int at = 0;
     for (int r0 = 0; r0 < p.rows_out; r0 += T) {
         const int r = r0 + threadIdx.x;
@@ -339,10 +355,9 @@ __device__ __forceinline__ int fork_list(const ForkParams& p) {
     }
     return at;
 }
-// The k-th fresh page.
-__device__ __forceinline__ void fork_give(const ForkParams& p, long long id, long long k) {
-    const int r = p.ws.rows[pg::MAX_ROWS + k], par = p.parent[r], page = static_cast<int>(id);
-    const int j = pg::pages_of(p.lens[par], p.shift, p.max_pages) - 1;
+// Row r's fresh page.
+__device__ __forceinline__ void fork_give(const ForkParams& p, int r, int page) {
+    const int par = p.parent[r], j = pg::pages_of(p.lens[par], p.shift, p.max_pages) - 1;
     p.out_table[static_cast<size_t>(r) * p.max_pages + j] = page;
     p.copy_src[r] = p.table[static_cast<size_t>(par) * p.max_pages + j];
     p.copy_dst[r] = page;
@@ -351,9 +366,9 @@ __device__ __forceinline__ void fork_give(const ForkParams& p, long long id, lon
 // The pool is used up after `got` pages: the rows at the end of the list keep
 // their full pages.
 template <int T>
-__device__ __forceinline__ void fork_short(const ForkParams& p, int got, int need, int pool_bit) {
+__device__ __forceinline__ void fork_short(const ForkParams& p, const int* list, int got, int need, int pool_bit) {
     for (int k = got + threadIdx.x; k < need; k += T) {
-        const int r = p.ws.rows[pg::MAX_ROWS + k];
+        const int r = list[k];
         p.out_lens[r] = p.lens[p.parent[r]] & ~((1 << p.shift) - 1);
     }
     if (threadIdx.x == 0) p.ws.head->status = pool_bit;
@@ -366,7 +381,7 @@ __global__ void __launch_bounds__(pg::THREADS) fork_count_kernel(const ForkParam
     pdl_wait_primary();
     const int tid = threadIdx.x;
     if (static_cast<int>(blockIdx.x) == p.pool.chunks) {
-        const int n = fork_list<THREADS>(p);
+        const int n = fork_list<THREADS>(p, p.ws.rows + MAX_ROWS);
         if (tid == 0) p.ws.head->need_list = n;
         return;
     }
@@ -380,23 +395,28 @@ __global__ void __launch_bounds__(pg::THREADS) fork_assign_kernel(const ForkPara
     const int chunk = blockIdx.x;
     const int need = p.ws.head->need_list;
     if (need == 0) return;
-    const uint64_t bits =
-        free_bits<RUN>(p.pool, chunk * p.pool.chunk + RUN * threadIdx.x, chunk_end(p.pool, chunk), RUN);
+    const unsigned bits = free_bits(p.pool, chunk * p.pool.chunk + RUN * threadIdx.x, chunk_end(p.pool, chunk));
+    const int* list = p.ws.rows + MAX_ROWS;
     const uint2 f = free_before(p.ws, p.pool.chunks, chunk);
-    if (chunk == 0 && f.y < static_cast<unsigned>(need)) fork_short<THREADS>(p, f.y, need, pool_bit);
-    hand_out_chunk(p.pool, chunk, bits, f.x, need, [&](long long id, long long k) { fork_give(p, id, k); });
+    if (chunk == 0 && f.y < static_cast<unsigned>(need)) fork_short<THREADS>(p, list, f.y, need, pool_bit);
+    hand_out_chunk(p.pool, chunk, bits, f.x, need,
+                   [&](long long id, long long k) { fork_give(p, list[k], static_cast<int>(id)); });
 }
 
 // Both for a small pool.
-__global__ void __launch_bounds__(pg::ONE_THREADS) fork_assign_small_kernel(const ForkParams p, const int pool_bit) {
+__global__ void __cluster_dims__(pg::SMALL_BLOCKS, 1, 1) __launch_bounds__(pg::SMALL_THREADS)
+    fork_assign_small_kernel(const ForkParams p, const int pool_bit) {
     using namespace pg;
+    __shared__ int s_rows[MAX_ROWS];
+    const int block = blockIdx.x;
     pdl_wait_primary();
-    const Small s = look_small(p.pool);
-    const int need = fork_list<ONE_THREADS>(p);
-    __syncthreads();   // the list, in global memory, is this block's own
-    if (s.total < need) fork_short<ONE_THREADS>(p, s.total, need, pool_bit);
-    hand_out<ONE_THREADS>(s.bits, s.mine, s.rank, s.total < need ? s.total : need, 0,
-                          [&](long long id, long long k) { fork_give(p, id, k); });
+    const Small s = look_small(p.pool, block);
+    const int need = fork_list<SMALL_THREADS>(p, s_rows);   // in every block
+    const uint2 f = cluster_sum(s.sum, block);
+    const int before = static_cast<int>(f.x), total = static_cast<int>(f.y);
+    if (block == 0 && total < need) fork_short<SMALL_THREADS>(p, s_rows, total, need, pool_bit);
+    hand_out<SMALL_THREADS>(s.bits, s.mine, s.rank, min(s.sum, need - before), before,
+                            [&](long long id, long long k) { fork_give(p, s_rows[k], static_cast<int>(id)); });
 }
 
 // ---------------------------------------------------------------------------
@@ -509,8 +529,8 @@ __global__ void __launch_bounds__(pg::THREADS)
     const bool pool_block = chunk < p.pool.chunks;
     // The counts change in this kernel only, a chunk by its own block.  Pages are
     // usually found in the first chunks, which look early.
-    uint64_t bits = 0;
-    auto look = [&] { bits = free_bits<RUN>(p.pool, chunk * p.pool.chunk + RUN * tid, chunk_end(p.pool, chunk), RUN); };
+    unsigned bits = 0;
+    auto look = [&] { bits = free_bits(p.pool, chunk * p.pool.chunk + RUN * tid, chunk_end(p.pool, chunk)); };
     if (pool_block && chunk < EARLY_CHUNKS) look();
     pdl_wait_primary();
     const int need = p.ws.head->need;
@@ -536,24 +556,28 @@ __global__ void __launch_bounds__(pg::THREADS)
 }
 
 // Both for a small pool.
-__global__ void __launch_bounds__(pg::ONE_THREADS)
+__global__ void __cluster_dims__(pg::SMALL_BLOCKS, 1, 1) __launch_bounds__(pg::SMALL_THREADS)
     extend_small_kernel(const ExtendParams p, const int pool_bit, const int row_bit) {
     using namespace pg;
     __shared__ int s_prefix[MAX_ROWS], s_len[MAX_ROWS];
-    const Small s = look_small(p.pool);
+    const int tid = threadIdx.x, block = blockIdx.x;
+    const Small s = look_small(p.pool, block);
     bool over;
-    const int need = extend_rows<ONE_THREADS>(p, &over, [&](int r, int len, int before) {
+    const int need = extend_rows<SMALL_THREADS>(p, &over, [&](int r, int len, int before) {   // in every block
         s_len[r] = len;
         s_prefix[r] = before;
-    });   // its last barrier covers the tables
-    const bool enough = need <= s.total, ok = !over && enough;
-    if (threadIdx.x == 0) p.ws.head->status = (over ? row_bit : 0) | (enough ? 0 : pool_bit);
-    extend_tokens(p, threadIdx.x, ONE_THREADS, ok, [&](int r) { return s_len[r]; });
+    });
+    const uint2 f = cluster_sum(s.sum, block);   // and every block has read the lengths
+    const int before = static_cast<int>(f.x);
+    const bool enough = need <= static_cast<int>(f.y), ok = !over && enough;
+    if (block == 0 && tid == 0) p.ws.head->status = (over ? row_bit : 0) | (enough ? 0 : pool_bit);
+    extend_tokens(p, block * SMALL_THREADS + tid, SMALL_BLOCKS * SMALL_THREADS, ok, [&](int r) { return s_len[r]; });
     if (!ok) return;
-    for (int r = threadIdx.x; r < p.rows; r += ONE_THREADS)
-        if (s_len[r] >= 0) p.lens[r] = s_len[r] + p.L;
-    hand_out<ONE_THREADS>(s.bits, s.mine, s.rank, need, 0,
-                          [&](long long page, long long k) { extend_give(p, s_prefix, s_len, page, k); });
+    if (block == 0)
+        for (int r = tid; r < p.rows; r += SMALL_THREADS)
+            if (s_len[r] >= 0) p.lens[r] = s_len[r] + p.L;
+    hand_out<SMALL_THREADS>(s.bits, s.mine, s.rank, min(s.sum, need - before), before,
+                            [&](long long page, long long k) { extend_give(p, s_prefix, s_len, page, k); });
 }
 
 // ---------------------------------------------------------------------------
@@ -640,13 +664,31 @@ __device__ __forceinline__ void compact_page(const CompactParams& p, const Moves
     }
 }
 
+// The pages [i, end) of a block (RUN a thread), `before` free ones before them:
+// neighbouring threads write neighbouring places, page by page and not run by run.
+template <int T>
+__device__ __forceinline__ void compact_pages(const CompactParams& p, const Moves& m, long long i, long long end,
+                                              long long before, unsigned bits, int rank) {
+    using namespace pg;
+    __shared__ uint16_t s_bits[T];
+    __shared__ int s_rank[T];
+    static_assert(RUN <= 16, "a run's bits");
+    s_bits[threadIdx.x] = static_cast<uint16_t>(bits);   // the last readers are behind a barrier of block_scan
+    s_rank[threadIdx.x] = rank;
+    __syncthreads();
+#pragma unroll 4
+    for (int o = threadIdx.x; o < T * RUN; o += T) {
+        const unsigned b = s_bits[o / RUN], at = o % RUN;
+        if (i + o < end)
+            compact_page(p, m, i + o, before + s_rank[o / RUN] + __popc(b & ((1u << at) - 1)), b >> at & 1);
+    }
+}
+
 __global__ void __launch_bounds__(pg::THREADS) compact_rank_kernel(const CompactParams p) {
     using namespace pg;
-    __shared__ uint16_t s_bits[THREADS];
-    __shared__ int s_rank[THREADS];
     const int tid = threadIdx.x, chunk = blockIdx.x;
     const long long i0 = chunk * p.pool.chunk, i1 = chunk_end(p.pool, chunk);
-    uint64_t bits = free_bits<RUN>(p.pool, i0 + RUN * tid, i1, RUN);   // the counts change in the next kernel only
+    unsigned bits = free_bits(p.pool, i0 + RUN * tid, i1);   // the counts change in the next kernel only
     pdl_launch_dependents();
     pdl_wait_primary();
     const uint2 f = free_before(p.ws, p.pool.chunks, chunk);
@@ -666,47 +708,31 @@ __global__ void __launch_bounds__(pg::THREADS) compact_rank_kernel(const Compact
     }
     long long before = f.x;   // free pages before the next ones
     for (long long i = i0; i < i1; i += CHUNK) {
-        if (i != i0) bits = free_bits<RUN>(p.pool, i + RUN * tid, i1, RUN);
+        if (i != i0) bits = free_bits(p.pool, i + RUN * tid, i1);
         int sum;
-        const int rank = block_scan<THREADS>(__popcll(bits), &sum);
-        // neighbouring threads write neighbouring places: page by page, not run by run
-        s_bits[tid] = static_cast<uint16_t>(bits);
-        s_rank[tid] = rank;
-        __syncthreads();
-#pragma unroll 4
-        for (int o = tid; o < CHUNK; o += THREADS) {
-            const unsigned b = s_bits[o / RUN], at = o % RUN;
-            if (i + o < i1)
-                compact_page(p, m, i + o, before + s_rank[o / RUN] + __popc(b & ((1u << at) - 1)), b >> at & 1);
-        }
+        const int rank = block_scan<THREADS>(__popc(bits), &sum);
+        compact_pages<THREADS>(p, m, i, i1, before, bits, rank);
         before += sum;
     }
 }
-static_assert(pg::RUN <= 16, "a run's bits");
-
 // Both for a small pool.
-__global__ void __launch_bounds__(pg::ONE_THREADS) compact_small_kernel(const CompactParams p) {
+__global__ void __cluster_dims__(pg::SMALL_BLOCKS, 1, 1) __launch_bounds__(pg::SMALL_THREADS)
+    compact_small_kernel(const CompactParams p) {
     using namespace pg;
-    __shared__ uint64_t s_bits[ONE_THREADS];
-    __shared__ int s_rank[ONE_THREADS];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, block = blockIdx.x;
     pdl_launch_dependents();
-    const Small s = look_small(p.pool);
-    const long long total = p.pool.num_pages - s.total;
-    const long long below = total - s.mine;   // the thread's pages below `total`
-    const uint64_t low = below >= 64 ? s.bits : below > 0 ? s.bits & ((1ull << below) - 1) : 0;
-    const Moves m = compact_moves(p, total, block_sum2<ONE_THREADS>(__popcll(low), 0).x);
-    if (tid == 0) compact_head(p, m);
-    for (int k = m.moves + tid; k < p.max_moves; k += ONE_THREADS) p.copy_src[k] = p.copy_dst[k] = -1;
-    s_bits[tid] = s.bits;
-    s_rank[tid] = s.rank;
-    __syncthreads();
-    const int run = static_cast<int>((p.pool.num_pages + 4 * ONE_THREADS - 1) / (4 * ONE_THREADS) * 4);
-    for (int id = tid; id < p.pool.num_pages; id += ONE_THREADS) {
-        const int who = id / run, at = id - who * run;
-        const uint64_t b = s_bits[who];
-        compact_page(p, m, id, s_rank[who] + __popcll(b & ((1ull << at) - 1)), b >> at & 1);
-    }
+    const Small s = look_small(p.pool, block);
+    const uint2 f = cluster_sum(s.sum, block);
+    const int total = static_cast<int>(p.pool.num_pages - f.y);
+    const int below = total - s.mine;   // the thread's pages below `total`
+    const unsigned low = below >= RUN ? s.bits : below > 0 ? s.bits & ((1u << below) - 1) : 0;
+    const unsigned mine = block_sum2<SMALL_THREADS>(__popc(low), 0).x;
+    const Moves m = compact_moves(p, total, cluster_sum(mine, block).y);
+    if (block == 0 && tid == 0) compact_head(p, m);
+    for (long long k = m.moves + block * SMALL_THREADS + tid; k < p.max_moves; k += SMALL_BLOCKS * SMALL_THREADS)
+        p.copy_src[k] = p.copy_dst[k] = -1;
+    const int i = block * SMALL_THREADS * RUN;
+    if (i < p.pool.num_pages) compact_pages<SMALL_THREADS>(p, m, i, p.pool.num_pages, f.x, s.bits, s.rank);
 }
 
 // Block y < rows: the row's entries follow their pages.  Block y == rows: so do
@@ -716,8 +742,8 @@ __global__ void __launch_bounds__(pg::THREADS) compact_apply_kernel(const Compac
     const bool counts = static_cast<int>(blockIdx.y) == p.rows;
     const int n = counts ? 0 : pages_of(p.lens[blockIdx.y], p.shift, p.max_pages);
     const long long stride = static_cast<long long>(gridDim.x) * THREADS, j00 = blockIdx.x * THREADS + threadIdx.x;
-    pdl_wait_primary();
     if (counts) {
+        pdl_wait_primary();
         const int moves = p.ws.head->moves;
         for (long long k = j00; k < moves; k += stride) {
             const int s = p.copy_src[k], d = p.copy_dst[k];
@@ -726,17 +752,21 @@ __global__ void __launch_bounds__(pg::THREADS) compact_apply_kernel(const Compac
         }
         return;
     }
-    const int total = p.ws.head->total;
     int* row = p.table + static_cast<size_t>(blockIdx.y) * p.max_pages;
+    bool waited = false;
     for (long long j0 = j00; j0 < n; j0 += 4 * stride) {   // four chains of loads at a time
         int page[4], k[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) page[u] = j0 + u * stride < n ? row[j0 + u * stride] : -1;
+        if (!waited) pdl_wait_primary();   // the tables change in this kernel only
+        waited = true;
+        const int total = p.ws.head->total;
+        // ranks below `total` were not written: what is read there is not used
 #pragma unroll
-        for (int u = 0; u < 4; ++u) k[u] = page[u] >= total && page[u] < p.pool.num_pages ? p.ws.rank[page[u]] : -1;
+        for (int u = 0; u < 4; ++u) k[u] = page[u] >= 0 && page[u] < p.pool.num_pages ? p.ws.rank[page[u]] : -1;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (k[u] >= 0) row[j0 + u * stride] = p.copy_dst[k[u]];
+            if (page[u] >= total && k[u] >= 0) row[j0 + u * stride] = p.copy_dst[k[u]];
     }
 }
 

@@ -208,7 +208,7 @@ __device__ __forceinline__ uint32_t idesc(const Params& p, int m, int n) {
 }
 
 // ---- linear_narrow_kernel's shared memory ----
-constexpr int NARROW_THREADS = 128;
+constexpr int NARROW_THREADS = 256;
 constexpr int NARROW_MAX_STAGES = 12;
 constexpr int RED_PITCH = ROWS + 4;                       // floats per token of the partial sums
 __host__ __device__ constexpr int narrow_stage(int tt) { return TILE + tt * BK * 2; }
@@ -234,6 +234,51 @@ constexpr int WIDE_BARS = 2 * WIDE_STAGES + 5;            // full, empty, 2 tile
 constexpr int WIDE_SMEM = 1024 + WIDE_STAGES * WIDE_STAGE + WIDE_EPI + 8 * WIDE_BARS + 8;
 constexpr int WIDE_GROUP = 8;                             // token tiles that share a sweep over N
 
+}  // namespace lin
+
+namespace lin {
+// The block's share (1 / S of the tokens x 128 rows) of a narrow tile: the
+// cluster's partial sums, in rank order, and the epilogue.  Several items' loads
+// are in flight at a time: those from other blocks take about 500 cycles.
+template <int S>
+__device__ __forceinline__ void narrow_finish(const Params& p, uint32_t red, int rank, int n0, int t0, int tn) {
+    constexpr int U = S >= 8 ? 1 : S >= 4 ? 2 : 4;
+    uint32_t base[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) base[s] = in_block(red, s);
+    const int items = tn * (ROWS / 4);
+    const int i0 = static_cast<int>(static_cast<long long>(items) * rank / S);
+    const int i1 = static_cast<int>(static_cast<long long>(items) * (rank + 1) / S);
+    for (int ii = i0 + static_cast<int>(threadIdx.x); ii < i1; ii += U * NARROW_THREADS) {
+        float4 q[U][S];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = ii + u * NARROW_THREADS;
+            if (i >= i1) continue;
+            const uint32_t at = static_cast<uint32_t>(i / (ROWS / 4) * RED_PITCH + i % (ROWS / 4) * 4) * 4u;
+#pragma unroll
+            for (int s = 0; s < S; ++s) q[u][s] = ld_cluster_f4(base[s] + at);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = ii + u * NARROW_THREADS;
+            const int t = i / (ROWS / 4), n = n0 + i % (ROWS / 4) * 4;
+            if (i >= i1 || n >= p.N) continue;
+            float v[4] = {q[u][0].x, q[u][0].y, q[u][0].z, q[u][0].w};
+#pragma unroll
+            for (int s = 1; s < S; ++s) {
+                v[0] += q[u][s].x; v[1] += q[u][s].y; v[2] += q[u][s].z; v[3] += q[u][s].w;
+            }
+            if (p.bias != nullptr) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < p.N) v[e] += load16(p.bias, n + e, p.fp16);
+            }
+            activate(v, p.act);
+            store4(p, t0 + t, n, v);
+        }
+    }
+}
 }  // namespace lin
 
 __global__ void __launch_bounds__(lin::NARROW_THREADS)
@@ -323,45 +368,31 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS)
     tc_fence_after();
     __syncthreads();   // the loads have landed (warp 0) and the MMAs are done: the ring is free
 
-    // ---- partial sums to shared memory: red[t][n], lane = weight row ----
+    // ---- partial sums to shared memory: red[t][n], lane = weight row; a warp
+    // reads the 32 rows that its number allows, every other 32 tokens ----
     const int tn = p.T - t0 < p.tt ? p.T - t0 : p.tt;      // the tile's tokens
     float* red = reinterpret_cast<float*>(smem);
     if (__all_sync(0xffffffffu, done && !*abort_flag)) {
-        const uint32_t row = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+        const int quad = warp & 3;
+        const uint32_t row = tmem + (static_cast<uint32_t>(32 * quad) << 16);
         uint32_t v[32];
-        for (int c0 = 0; c0 < tn; c0 += 32) {
+        for (int c0 = 32 * (warp >> 2); c0 < tn; c0 += 64) {
             tc_ld32(row + static_cast<uint32_t>(c0), v);
             tc_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (c0 + j < tn) red[(c0 + j) * RED_PITCH + 32 * warp + lane] = __uint_as_float(v[j]);
+                if (c0 + j < tn) red[(c0 + j) * RED_PITCH + 32 * quad + lane] = __uint_as_float(v[j]);
         }
     }
     tc_fence_before();
     cluster_sync();
 
     // ---- this block's share of the tile: sum over the cluster, epilogue ----
-    {
-        const int items = tn * (ROWS / 4);
-        const int i0 = static_cast<int>(static_cast<long long>(items) * rank / split);
-        const int i1 = static_cast<int>(static_cast<long long>(items) * (rank + 1) / split);
-        for (int i = i0 + tid; i < i1; i += NARROW_THREADS) {
-            const int t = i / (ROWS / 4), c = i % (ROWS / 4) * 4, n = n0 + c;
-            if (n >= p.N) continue;
-            const uint32_t at = ring + static_cast<uint32_t>(t * RED_PITCH + c) * 4u;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int s = 0; s < split; ++s) {
-                const float4 q = ld_cluster_f4(in_block(at, s));
-                v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
-            }
-            if (p.bias != nullptr) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (n + u < p.N) v[u] += load16(p.bias, n + u, p.fp16);
-            }
-            activate(v, p.act);
-            store4(p, t0 + t, n, v);
-        }
+    switch (split) {
+        case 1: narrow_finish<1>(p, ring, rank, n0, t0, tn); break;
+        case 2: narrow_finish<2>(p, ring, rank, n0, t0, tn); break;
+        case 4: narrow_finish<4>(p, ring, rank, n0, t0, tn); break;
+        default: narrow_finish<8>(p, ring, rank, n0, t0, tn); break;
     }
     cluster_sync();   // the other blocks have read this one's sums
     if (warp == 1) {

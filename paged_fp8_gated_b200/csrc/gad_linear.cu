@@ -6,6 +6,9 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
+#include <mutex>
+
 #include "gad_host.h"
 #include "gad_linear.cuh"
 
@@ -70,90 +73,242 @@ constexpr int smem_share(int cols) {
 }
 static_assert(smem_share(512) == kSmemMax, "all of tensor memory, all of shared memory");
 
-int launch_narrow(gad::lin::Params p, const void* x, long long ldx, const void* w, long long ldw, int sms,
-                  cudaStream_t s) {
+constexpr int kClasses = 3;   // 1, 2 or 4 blocks per SM
+constexpr int kSplits = 4;    // clusters of 1, 2, 4 or 8
+
+// How a call runs.
+struct Plan {
+    enum Kind { NARROW, WIDE } kind = NARROW;
+    int bn = 0;        // wide: 256 or 128
+    int split = 1;     // narrow: blocks of a cluster; wide: pairs of a cluster
+    int cls = 0;       // narrow: 2^cls blocks per SM
+    bool promote = false;
+    double us = 1e30;
+};
+
+// Clusters that the GPU holds at a time: narrow[cls][log2 split], wide[log2 pairs].
+struct Capacity {
+    int narrow[kClasses][kSplits];
+    int wide[3];
+};
+
+int cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned blocks_x, unsigned blocks_y, int threads,
+                   int smem, int cluster, cudaStream_t s) {
+    std::memset(cfg, 0, sizeof(*cfg));
+    cfg->gridDim = dim3(blocks_x, blocks_y);
+    cfg->blockDim = dim3(static_cast<unsigned>(threads));
+    cfg->dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg->stream = s;
+    std::memset(attr, 0, sizeof(*attr));
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr->val.clusterDim.y = 1;
+    attr->val.clusterDim.z = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = 1;
+    return GAD_OK;
+}
+
+// Stands for the kernels in the question how many clusters fit: for a kernel that
+// allocates tensor memory the answer counts one block per SM whatever its shared
+// memory, though the blocks do run side by side (threads and registers, at most
+// 64 in the four-block class, allow it).
+__global__ void __launch_bounds__(256) resident_probe_kernel() {}
+
+int capacity_of(OncePerContext& once, int smem, int cluster, int* out) {
+    const int st = raise_smem(reinterpret_cast<const void*>(resident_probe_kernel), once, kSmemMax);
+    if (st != GAD_OK) return st;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    cluster_config(&cfg, &attr, static_cast<unsigned>(4096 * cluster), 1, 256, smem, cluster, nullptr);
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(out, resident_probe_kernel, &cfg);
+    if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "cudaOccupancyMaxActiveClusters: %s", cudaGetErrorString(e));
+    if (*out < 1) *out = 1;
+    return GAD_OK;
+}
+
+OncePerContext g_narrow_smem[4], g_wide_smem[8];
+
+// Asked once per (device, context).
+int capacity(const Capacity** out) {
+    static OncePerContext asked, raised;
+    static Capacity cap[kMaxDevices];
+    static std::mutex lock;
+    int dev = 0;
+    const int ds = current_device(&dev);
+    if (ds != GAD_OK) return ds;
+    *out = &cap[dev];
+    if (asked.is_done(dev, current_ctx_id())) return GAD_OK;
+    const std::lock_guard<std::mutex> hold(lock);
+    if (asked.is_done(dev, current_ctx_id())) return GAD_OK;
+    Capacity c;
+    for (int m = 0; m < kClasses; ++m)
+        for (int k = 0; k < kSplits; ++k) {
+            const int st = capacity_of(raised, smem_share(512 >> m), 1 << k, &c.narrow[m][k]);
+            if (st != GAD_OK) return st;
+        }
+    for (int k = 0; k < 3; ++k) {
+        const int st = capacity_of(raised, smem_share(512), 2 << k, &c.wide[k]);
+        if (st != GAD_OK) return st;
+    }
+    cap[dev] = c;
+    asked.mark(dev);
+    return GAD_OK;
+}
+
+// Tokens per narrow tile: as even as tiles of at most 256 can be.
+int narrow_tokens(int T) {
+    const int tiles = (T + 255) / 256;
+    return ((T + tiles - 1) / tiles + 15) / 16 * 16;
+}
+
+// A chain of more than this many stages is promoted for a fp32 result.
+constexpr int kLongChain = 768 / gad::lin::BK;
+
+// The plan with the least time by this model of the kernels, in microseconds.
+// Its constants are fitted to both kernels at T = 1 .. 4,096 over nine (K, N)
+// from 256 x 32,000 to 8,192 x 32,001, cold weights:
+//   narrow: a stage takes a block 0.30 (an SM draws 54 GB/s of weights), or its
+//     bytes at an SM's 123 GB/s from L2, or all blocks' weights at 6.4 TB/s, or
+//     a load's latency (2.0) over the stages in flight; a
+//     block's fixed part is its cluster's start, its share of the epilogue and
+//     the exchange with the cluster.  Example (cold weights): 32 x
+//     8,192 x 2,304 (18 tiles) 42 / 23 / 14 / 12 in clusters of 1 / 2 / 4 / 8.
+//   wide: a stage of 256 x 256 takes a pair 0.33 (the tensor cores' time; 0.41
+//     when no other tile reads the same weights), one of 256 x 128 0.25 (an SM's
+//     share of L2 bandwidth).  Example: 768 x 8,192 x
+//     2,304 44 on 27 of 74 pairs, 29 with two pairs a tile; 1,024 x 8,192 x 2,304
+//     (36 tiles, more than the 33 clusters of four blocks that fit) 44 and 55.
+Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
     using namespace gad::lin;
-    const int token_tiles = (p.T + 255) / 256;
-    p.tt = ((p.T + token_tiles - 1) / token_tiles + 15) / 16 * 16;
-    const long long tiles = static_cast<long long>((p.N + ROWS - 1) / ROWS) * token_tiles;
-    const int nk = (p.K + BK - 1) / BK;
-    // Blocks that share a tile's K range: the count with the least work on the
-    // busiest SM, a block's fixed part counted as four stages.
-    int split = 1;
-    long long best = -1;
-    for (int c = 1; c <= 8 && c <= nk; c *= 2) {
-        const long long cost = (tiles * c + sms - 1) / sms * ((nk + c - 1) / c + 4);
-        if (best < 0 || cost < best) {
-            best = cost;
-            split = c;
+    const int nk = (K + BK - 1) / BK;
+    Plan best;
+    auto take = [&](const Plan& q) {
+        if (q.us < best.us) best = q;
+    };
+    const double dram = 2.0 * (static_cast<double>(T) * K + static_cast<double>(N) * K) / 6.4e6;
+    {
+        const int tt = narrow_tokens(T);
+        const long long tiles = static_cast<long long>((T + tt - 1) / tt) * ((N + ROWS - 1) / ROWS);
+        for (int k = 0; k < kSplits && (1 << k) <= nk; ++k) {
+            const int c = 1 << k, own = (nk + c - 1) / c;
+            const bool promote = f32 && own > kLongChain;
+            for (int m = 0; m < kClasses; ++m) {
+                const int budget = smem_share(512 >> m);
+                if (narrow_cols(tt) * (promote ? 2 : 1) > 512 >> m || narrow_smem(tt, 1) > budget) continue;
+                if (promote && m > 1) continue;   // registers for two blocks
+                int stages = 1;
+                while (stages < own && stages < NARROW_MAX_STAGES && narrow_smem(tt, stages + 1) <= budget) ++stages;
+                const double fixed = 1.0 + 0.15 * c + tt * (0.012 + 0.016 / c + 0.004 * c);
+                auto wave = [&](double clusters) {
+                    const double blocks = clusters * c, per_sm = std::fmax(1.0, std::ceil(blocks / sms));
+                    double ts = std::fmax(0.30, per_sm * narrow_stage(tt) / 123e3);
+                    ts = std::fmax(ts, blocks * TILE / 6.4e6);
+                    if (own > stages) ts = std::fmax(ts, 2.0 / stages);
+                    return own * ts + fixed;
+                };
+                const long long fit = cap.narrow[m][k], full = tiles / fit, rest = tiles % fit;
+                Plan q;
+                q.kind = Plan::NARROW;
+                q.split = c;
+                q.cls = m;
+                q.promote = promote;
+                q.us = 2.4 + full * wave(static_cast<double>(fit)) + (rest ? wave(static_cast<double>(rest)) : 0.0);
+                take(q);
+            }
         }
     }
-    // the ring: all of an SM's shared memory when there is a block per SM at
-    // most (or the partial sums need it), else half of it
-    const int half = smem_share(256);
-    const int budget = tiles * split <= sms || narrow_smem(p.tt, 0) > half ? kSmemMax : half;
-    const int own_nk = (nk + split - 1) / split;
-    p.nstg = 1;
-    while (p.nstg < NARROW_MAX_STAGES && p.nstg < own_nk && narrow_smem(p.tt, p.nstg + 1) <= budget) ++p.nstg;
-    int smem = narrow_smem(p.tt, p.nstg);
-    const int share = smem_share(static_cast<int>(narrow_cols(p.tt)));
-    if (smem < share) smem = share;
-    if (smem > kSmemMax) return fail(GAD_ERR_SHAPE, "linear ring of %d bytes", smem);   // never launched
+    const double stage256 = T <= 256 ? 0.41 : 0.33;
+    for (int bn = 256; bn >= 128; bn /= 2) {
+        const double tiles = std::ceil(T / 256.0) * std::ceil(static_cast<double>(N) / bn);
+        for (int k = 0; k < 3 && (1 << k) <= nk; ++k) {
+            const int own = (nk + (1 << k) - 1) >> k;
+            const bool promote = f32 && own > kLongChain;
+            if (promote && bn != 128) continue;
+            Plan q;
+            q.kind = Plan::WIDE;
+            q.bn = bn;
+            q.split = 1 << k;
+            q.promote = promote;
+            const double waves = std::ceil(tiles / cap.wide[k]);
+            if (k == 0)
+                q.us = bn == 256 ? 6.7 + waves * std::fmax(own * stage256, 3.0) : 5.0 + waves * std::fmax(own * 0.25, 1.9);
+            else
+                q.us = 3.5 + waves * (bn == 256 ? own * stage256 + 5.3 : own * 0.22 + 2.5);
+            q.us = std::fmax(q.us, 3.5 + dram);
+            take(q);
+        }
+    }
+    return best;
+}
 
-    static OncePerContext attr_done;
-    int st = raise_smem(reinterpret_cast<const void*>(gad::linear_narrow_kernel), attr_done, kSmemMax);
+template <int ACC>
+int launch_narrow(gad::lin::Params p, const void* x, long long ldx, const void* w, long long ldw, const Plan& plan,
+                  cudaStream_t s) {
+    using namespace gad::lin;
+    auto kern = gad::linear_narrow_kernel<ACC>;
+    p.tt = narrow_tokens(p.T);
+    const int token_tiles = (p.T + p.tt - 1) / p.tt, nk = (p.K + BK - 1) / BK;
+    const int budget = smem_share(512 >> plan.cls), own = (nk + plan.split - 1) / plan.split;
+    p.nstg = 1;
+    while (p.nstg < NARROW_MAX_STAGES && p.nstg < own && narrow_smem(p.tt, p.nstg + 1) <= budget) ++p.nstg;
+    if (narrow_smem(p.tt, p.nstg) > budget || narrow_cols(p.tt) * (ACC ? 2 : 1) > 512 >> plan.cls)
+        return fail(GAD_ERR_SHAPE, "linear tile of %d tokens does not fit", p.tt);   // choose() plans none such
+    int st = raise_smem(reinterpret_cast<const void*>(kern), g_narrow_smem[ACC / 32 > 2 ? 3 : ACC / 32], kSmemMax);
     if (st != GAD_OK) return st;
     CUtensorMap wmap, xmap;
     st = encode_rows(&wmap, w, p.fp16 != 0, p.K, p.N, ldw, ROWS);
     if (st == GAD_OK) st = encode_rows(&xmap, x, p.fp16 != 0, p.K, p.T, ldx, p.tt);
     if (st != GAD_OK) return st;
     cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>((p.N + ROWS - 1) / ROWS * split), static_cast<unsigned>(token_tiles));
-    cfg.blockDim = dim3(NARROW_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
     cudaLaunchAttribute attr[2];
-    attr[0] = pdl_attr();
-    std::memset(&attr[1], 0, sizeof(attr[1]));
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = split;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
+    cluster_config(&cfg, attr, static_cast<unsigned>((p.N + ROWS - 1) / ROWS * plan.split),
+                   static_cast<unsigned>(token_tiles), NARROW_THREADS<ACC>, budget, plan.split, s);
+    attr[1] = pdl_attr();
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gad::linear_narrow_kernel, wmap, xmap, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, wmap, xmap, p);
     if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));
     return GAD_OK;
 }
 
-int launch_wide(gad::lin::Params p, const void* x, long long ldx, const void* w, long long ldw, int sms,
+template <int BN, bool SPLIT, bool PROMOTE>
+int launch_wide(gad::lin::Params p, const void* x, long long ldx, const void* w, long long ldw, const Plan& plan, int sms,
                 cudaStream_t s) {
     using namespace gad::lin;
-    static OncePerContext attr_done;
-    int st = raise_smem(reinterpret_cast<const void*>(gad::linear_wide_kernel), attr_done, kSmemMax);
+    auto kern = gad::linear_wide_kernel<BN, SPLIT, PROMOTE>;
+    static_assert(Wide<BN, SPLIT, PROMOTE>::SMEM <= kSmemMax, "ring and staging fit");
+    int st = raise_smem(reinterpret_cast<const void*>(kern), g_wide_smem[(BN == 256) + 2 * SPLIT + 4 * PROMOTE], kSmemMax);
     if (st != GAD_OK) return st;
     p.mt = (p.T + 255) / 256;
-    p.nt = (p.N + 255) / 256;
+    p.nt = (p.N + BN - 1) / BN;
+    p.split = plan.split;
     const long long tiles = static_cast<long long>(p.mt) * p.nt;
     CUtensorMap wmap, xmap;
-    st = encode_rows(&wmap, w, p.fp16 != 0, p.K, p.N, ldw, ROWS);
+    st = encode_rows(&wmap, w, p.fp16 != 0, p.K, p.N, ldw, BN / 2);
     if (st == GAD_OK) st = encode_rows(&xmap, x, p.fp16 != 0, p.K, p.T, ldx, ROWS);
     if (st != GAD_OK) return st;
-    const long long pairs = tiles < sms / 2 ? tiles : sms / 2;
+    const long long pairs = SPLIT ? tiles * plan.split : tiles < sms / 2 ? tiles : sms / 2;
     cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-    cfg.blockDim = dim3(WIDE_THREADS);
-    static_assert(WIDE_SMEM <= kSmemMax, "ring and staging fit");
-    cfg.dynamicSmemBytes = smem_share(512);   // its pair holds all of tensor memory
-    cfg.stream = s;
-    cudaLaunchAttribute attr = pdl_attr();
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gad::linear_wide_kernel, wmap, xmap, p);
+    cudaLaunchAttribute attr[2];
+    // all of an SM's shared memory: alone there, so its tensor memory is free
+    cluster_config(&cfg, attr, static_cast<unsigned>(2 * pairs), 1, WIDE_THREADS, smem_share(512), 2 * plan.split, s);
+    attr[1] = pdl_attr();
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, wmap, xmap, p);
     if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));
     return GAD_OK;
+}
+
+template <bool PROMOTE>
+int launch_wide(const gad::lin::Params& p, const void* x, long long ldx, const void* w, long long ldw, const Plan& plan,
+                int sms, cudaStream_t s) {
+    if constexpr (!PROMOTE) {
+        if (plan.bn == 256)
+            return plan.split > 1 ? launch_wide<256, true, false>(p, x, ldx, w, ldw, plan, sms, s)
+                                  : launch_wide<256, false, false>(p, x, ldx, w, ldw, plan, sms, s);
+    }
+    return plan.split > 1 ? launch_wide<128, true, PROMOTE>(p, x, ldx, w, ldw, plan, sms, s)
+                          : launch_wide<128, false, PROMOTE>(p, x, ldx, w, ldw, plan, sms, s);
 }
 
 }  // namespace
@@ -207,12 +362,24 @@ int gad_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const voi
     p.out = out_dtype == GAD_DTYPE_F32 ? gad::lin::OUT_F32 : p.fp16 ? gad::lin::OUT_F16 : gad::lin::OUT_BF16;
     p.act = activation;
     p.vec = ldy % 4 == 0 && aligned(y, 4 * oe) && (!residual || (ldr % 4 == 0 && aligned(residual, 4 * oe)));
+    const int chunk = 16 / oe;
+    p.vec16 = ldy % chunk == 0 && aligned(y, 16) && (!residual || (ldr % chunk == 0 && aligned(residual, 16)));
     st = linear_status_word(&p.err);
     if (st != GAD_OK) return st;
-    const long long wide_tiles = static_cast<long long>((T + 255) / 256) * ((N + 255) / 256);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return T > 256 && wide_tiles >= sms / 4 ? launch_wide(p, x, ldx, w, ldw, sms, s)
-                                            : launch_narrow(p, x, ldx, w, ldw, sms, s);
+    const Capacity* cap = nullptr;
+    st = capacity(&cap);
+    if (st != GAD_OK) return st;
+    const Plan plan = choose(T, K, N, out_dtype == GAD_DTYPE_F32, *cap, sms);
+    if (plan.kind == Plan::WIDE)
+        return plan.promote ? launch_wide<true>(p, x, ldx, w, ldw, plan, sms, s)
+                            : launch_wide<false>(p, x, ldx, w, ldw, plan, sms, s);
+    if (!plan.promote) return launch_narrow<0>(p, x, ldx, w, ldw, plan, s);
+    switch (gad::lin::narrow_acc(narrow_tokens(T))) {
+        case 32: return launch_narrow<32>(p, x, ldx, w, ldw, plan, s);
+        case 64: return launch_narrow<64>(p, x, ldx, w, ldw, plan, s);
+        default: return launch_narrow<128>(p, x, ldx, w, ldw, plan, s);
+    }
 }
 
 int gad_linear_status(int* status, void* stream) {

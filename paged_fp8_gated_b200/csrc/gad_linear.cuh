@@ -17,10 +17,19 @@
 // sums meet in shared memory over the cluster, added in rank order (the result
 // does not depend on timing), and each block finishes a share of the tile.
 //
-// linear_wide_kernel: many tokens, bound by the tensor cores.  Persistent
-// pairs of blocks (cta_group::2), 256 x 256 tiles (each block holds 128 tokens
-// and 128 weight rows of a stage), two accumulators in tensor memory, so a
-// tile's epilogue runs beside the next tile's MMAs.
+// linear_wide_kernel: many tokens, bound by the tensor cores.  Pairs of blocks
+// (cta_group::2) on tiles of 256 tokens x BN weight rows (each block holds 128
+// tokens and BN / 2 weight rows of a stage).  Persistent, with two accumulators
+// in tensor memory, so that a tile's epilogue runs beside the next tile's MMAs;
+// or, where the tiles are few, SPLIT: one tile a cluster of up to four pairs
+// that share its K range and add their partial sums up in rank order, as the
+// narrow kernel does.
+//
+// Both can PROMOTE: the tensor cores cut the partial sum off at every step of
+// 16, so a chain of K products loses 1e-6 of the result per 1,024 (measured; a
+// 16-bit result does not see it).  For a fp32 result with a longer chain the
+// MMAs change accumulators every 512 products, and warps that are idle
+// otherwise add the finished one up in registers, rounding to nearest.
 #pragma once
 
 #include <cuda.h>
@@ -35,6 +44,7 @@ namespace lin {
 constexpr int BK = 64;                       // K per stage: one 128-byte row
 constexpr int ROWS = 128;                    // weight rows (narrow), tokens or weight rows of a block (wide)
 constexpr int TILE = ROWS * BK * 2;          // bytes of 128 rows of a stage
+constexpr int SEG = 512 / BK;                // stages of a chain that is promoted
 
 enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
 enum Out { OUT_BF16 = 0, OUT_F16 = 1, OUT_F32 = 2 };
@@ -48,8 +58,10 @@ struct Params {
     int fp16;                // x, w and bias are fp16 (else bf16)
     int out, act;            // Out, Act
     int vec;                 // y (and residual) take aligned stores of four values
+    int vec16;               // and of 16 bytes
     int tt, nstg;            // narrow: tokens per tile, ring stages
     int mt, nt;              // wide: tiles along the tokens and along N
+    int split;               // wide, SPLIT: pairs that share a tile
     int* err;                // status word: STATUS_LINEAR_WAIT when a bounded wait gave up
 };
 constexpr int STATUS_LINEAR_WAIT = 16;
@@ -131,13 +143,82 @@ __device__ __forceinline__ void store4(const Params& p, long long t, int n, cons
     }
 }
 
+template <int OUT>
+struct OutType;
+template <>
+struct OutType<OUT_F32> {
+    using type = float;
+    __device__ static float widen(float x) { return x; }
+    __device__ static float round(float x) { return x; }
+};
+template <>
+struct OutType<OUT_BF16> {
+    using type = __nv_bfloat16;
+    __device__ static float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+    __device__ static __nv_bfloat16 round(float x) { return __float2bfloat16(x); }
+};
+template <>
+struct OutType<OUT_F16> {
+    using type = __half;
+    __device__ static float widen(__half x) { return __half2float(x); }
+    __device__ static __half round(float x) { return __float2half(x); }
+};
+
+// Eight values to y's type in 16 (or 32) bytes; eight of the residual.
+template <int OUT>
+__device__ __forceinline__ void store8(void* y, size_t at, const float (&v)[8]) {
+    if (OUT == OUT_F32) {
+        float4* d = reinterpret_cast<float4*>(static_cast<float*>(y) + at);
+        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (OUT == OUT_BF16) {
+                __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<uint32_t*>(&b);
+            } else {
+                w[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
+            }
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+template <int OUT>
+__device__ __forceinline__ void add8(const void* r, size_t at, float (&v)[8]) {
+    if (OUT == OUT_F32) {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(r) + at);
+        const float4 a = q[0], b = q[1];
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    } else {
+        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(r) + at);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (OUT == OUT_BF16) {
+                v[2 * i] += __uint_as_float(w[i] << 16);
+                v[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                v[2 * i] += f.x;
+                v[2 * i + 1] += f.y;
+            }
+        }
+    }
+}
+
 // ---- thread-block clusters ----
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
     return r;
 }
+// (the aligned forms need the warp converged, which code with divergent loops
+// before them does not promise by itself)
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 // The address of `addr` (this block's shared memory) in block `rank` of the cluster.
@@ -169,12 +250,13 @@ __device__ __forceinline__ void tc2_relinquish() {
 __device__ __forceinline__ void tc2_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Arrives on `bar` in both blocks when the pair's MMAs issued so far are done.  Whole warp.
-__device__ __forceinline__ void tc2_commit_both(uint32_t bar) {
+// Arrives on `bar` in both blocks of the pair (cluster ranks first_block and
+// first_block + 1) when its MMAs issued so far are done.  Whole warp.
+__device__ __forceinline__ void tc2_commit_both(uint32_t bar, uint32_t first_block) {
     asm volatile(
         "{\n .reg .pred e;\n .reg .b32 rx;\n elect.sync rx|e, 0xffffffff;\n"
         " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
+        "h"(static_cast<uint16_t>(3u << first_block))
         : "memory");
 }
 // Four MMAs of K = 64: D (+)= A(a + 32 k bytes) B(b + 32 k bytes)^T, k = 0..3.  Whole warp, one lane issues.
@@ -208,8 +290,13 @@ __device__ __forceinline__ uint32_t idesc(const Params& p, int m, int n) {
 }
 
 // ---- linear_narrow_kernel's shared memory ----
-constexpr int NARROW_THREADS = 256;
+// ACC: accumulators that a thread promotes to (columns of tensor memory that
+// its warp reads), or 0.  Warps 0 and 1 load and issue; all eight read the
+// accumulator at the end, or with ACC eight others all along.
+template <int ACC>
+constexpr int NARROW_THREADS = ACC != 0 ? 320 : 256;
 constexpr int NARROW_MAX_STAGES = 12;
+constexpr int NARROW_BARS = 2 * NARROW_MAX_STAGES + 5;    // full, empty, done, 2 chain full, 2 chain empty
 constexpr int RED_PITCH = ROWS + 4;                       // floats per token of the partial sums
 __host__ __device__ constexpr int narrow_stage(int tt) { return TILE + tt * BK * 2; }
 __host__ __device__ constexpr int narrow_ring(int tt, int nstg) {  // ring, later the partial sums
@@ -217,22 +304,83 @@ __host__ __device__ constexpr int narrow_ring(int tt, int nstg) {  // ring, late
     return ring > red ? ring : red;
 }
 __host__ __device__ constexpr int narrow_smem(int tt, int nstg) {
-    return 1024 + narrow_ring(tt, nstg) + 8 * (2 * NARROW_MAX_STAGES + 1) + 8;
+    return 1024 + narrow_ring(tt, nstg) + 8 * NARROW_BARS + 8;
 }
-__host__ __device__ constexpr uint32_t narrow_cols(int tt) {
-    return tt <= 32 ? 32u : tt <= 64 ? 64u : tt <= 128 ? 128u : 256u;
-}
+__host__ __device__ constexpr int narrow_cols(int tt) { return tt <= 32 ? 32 : tt <= 64 ? 64 : tt <= 128 ? 128 : 256; }
+__host__ __device__ constexpr int narrow_acc(int tt) { return tt <= 64 ? 32 : tt <= 128 ? 64 : 128; }
 
 // ---- linear_wide_kernel's shared memory ----
-constexpr int WIDE_STAGES = 5;
 constexpr int WIDE_EPI_WARPS = 8;
 constexpr int WIDE_THREADS = 32 * (4 + WIDE_EPI_WARPS);
-constexpr int WIDE_STAGE = 2 * TILE;                      // 128 tokens and 128 weight rows
 constexpr int WIDE_PITCH = 36;                            // floats per row of an epilogue warp's 32 x 32 values
-constexpr int WIDE_EPI = WIDE_EPI_WARPS * 32 * WIDE_PITCH * 4;
-constexpr int WIDE_BARS = 2 * WIDE_STAGES + 5;            // full, empty, 2 tile full, 2 tile empty, done
-constexpr int WIDE_SMEM = 1024 + WIDE_STAGES * WIDE_STAGE + WIDE_EPI + 8 * WIDE_BARS + 8;
 constexpr int WIDE_GROUP = 8;                             // token tiles that share a sweep over N
+template <int BN, bool SPLIT, bool PROMOTE>
+struct Wide {
+    static constexpr int STAGES = BN == 256 ? 5 : 7;
+    static constexpr int STAGE = TILE + BN / 2 * BK * 2;  // 128 tokens and BN / 2 weight rows
+    static constexpr int EPI = WIDE_EPI_WARPS * 32 * WIDE_PITCH * 4;
+    static constexpr int BUFS = SPLIT && !PROMOTE ? 1 : 2;  // accumulators
+    static constexpr int BARS = 2 * STAGES + 5;           // full, empty, 2 tile full, 2 tile empty, done
+    static constexpr int SMEM = 1024 + STAGES * STAGE + EPI + 8 * BARS + 8;
+    static constexpr int PART_PITCH = BN + 4;             // SPLIT: floats per token of the partial sums
+    static_assert(!SPLIT || ROWS * PART_PITCH * 4 <= STAGES * STAGE, "the partial sums fit the ring");
+    static_assert(!PROMOTE || BN == 128, "64 sums a thread");
+};
+
+// A warp writes its 32 x 32 values (rows WIDE_PITCH floats apart in shared
+// memory) to rows t0 .. t0 + 31, columns n0 .. n0 + 31 of y, with the residual:
+// four lanes a row, 16 bytes of y each (32 in fp32), all loads before the stores.
+template <int OUT>
+__device__ __forceinline__ void write_tile(const Params& p, const float* tile, long long t0, int n0, int lane) {
+    const int r0 = lane >> 2, j = (lane & 3) * 8;
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 a = *reinterpret_cast<const float4*>(tile + (8 * i + r0) * WIDE_PITCH + j);
+        const float4 b = *reinterpret_cast<const float4*>(tile + (8 * i + r0) * WIDE_PITCH + j + 4);
+        v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+        v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
+    }
+    const int rows = p.T - t0 < 32 ? static_cast<int>(p.T - t0) : 32;
+    if (p.residual != nullptr) {
+        const size_t at = (t0 + r0) * p.ldr + n0 + j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (8 * i + r0 < rows) add8<OUT>(p.residual, at + 8 * i * p.ldr, v[i]);
+    }
+    const size_t at = (t0 + r0) * p.ldy + n0 + j;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (8 * i + r0 < rows) store8<OUT>(p.y, at + 8 * i * p.ldy, v[i]);
+}
+// The same at the edge of y and for rows that are not aligned: a lane a column.
+template <int OUT>
+__device__ __forceinline__ void write_edge(const Params& p, const float* tile, long long t0, int n0, int lane) {
+    using E = typename OutType<OUT>::type;
+    if (n0 + lane >= p.N) return;
+    const int rows = p.T - t0 < 32 ? static_cast<int>(p.T - t0) : 32;
+    const E* res = p.residual == nullptr ? nullptr : static_cast<const E*>(p.residual) + t0 * p.ldr + n0 + lane;
+    E* y = static_cast<E*>(p.y) + t0 * p.ldy + n0 + lane;
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = tile[(r0 + i) * WIDE_PITCH + lane];
+        if (res != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (r0 + i < rows) v[i] += OutType<OUT>::widen(res[(r0 + i) * p.ldr]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (r0 + i < rows) y[(r0 + i) * p.ldy] = OutType<OUT>::round(v[i]);
+    }
+}
+template <int OUT>
+__device__ __forceinline__ void write32(const Params& p, const float* tile, long long t0, int n0, int lane) {
+    if (t0 >= p.T) return;
+    if (p.vec16 && n0 + 32 <= p.N) write_tile<OUT>(p, tile, t0, n0, lane);
+    else write_edge<OUT>(p, tile, t0, n0, lane);
+}
 
 }  // namespace lin
 
@@ -240,7 +388,7 @@ namespace lin {
 // The block's share (1 / S of the tokens x 128 rows) of a narrow tile: the
 // cluster's partial sums, in rank order, and the epilogue.  Several items' loads
 // are in flight at a time: those from other blocks take about 500 cycles.
-template <int S>
+template <int S, int THREADS>
 __device__ __forceinline__ void narrow_finish(const Params& p, uint32_t red, int rank, int n0, int t0, int tn) {
     constexpr int U = S >= 8 ? 1 : S >= 4 ? 2 : 4;
     uint32_t base[S];
@@ -249,11 +397,11 @@ __device__ __forceinline__ void narrow_finish(const Params& p, uint32_t red, int
     const int items = tn * (ROWS / 4);
     const int i0 = static_cast<int>(static_cast<long long>(items) * rank / S);
     const int i1 = static_cast<int>(static_cast<long long>(items) * (rank + 1) / S);
-    for (int ii = i0 + static_cast<int>(threadIdx.x); ii < i1; ii += U * NARROW_THREADS) {
+    for (int ii = i0 + static_cast<int>(threadIdx.x); ii < i1; ii += U * THREADS) {
         float4 q[U][S];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = ii + u * NARROW_THREADS;
+            const int i = ii + u * THREADS;
             if (i >= i1) continue;
             const uint32_t at = static_cast<uint32_t>(i / (ROWS / 4) * RED_PITCH + i % (ROWS / 4) * 4) * 4u;
 #pragma unroll
@@ -261,7 +409,7 @@ __device__ __forceinline__ void narrow_finish(const Params& p, uint32_t red, int
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = ii + u * NARROW_THREADS;
+            const int i = ii + u * THREADS;
             const int t = i / (ROWS / 4), n = n0 + i % (ROWS / 4) * 4;
             if (i >= i1 || n >= p.N) continue;
             float v[4] = {q[u][0].x, q[u][0].y, q[u][0].z, q[u][0].w};
@@ -281,7 +429,8 @@ __device__ __forceinline__ void narrow_finish(const Params& p, uint32_t red, int
 }
 }  // namespace lin
 
-__global__ void __launch_bounds__(lin::NARROW_THREADS)
+template <int ACC>
+__global__ void __launch_bounds__(lin::NARROW_THREADS<ACC>, ACC == 0 ? 4 : ACC == 128 ? 1 : 2)
     linear_narrow_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
                          const lin::Params p) {
     using namespace lin;
@@ -296,8 +445,10 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS)
     auto FULL = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(s); };
     auto EMPTY = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(NSTG + s); };
     const uint32_t DONE = bar0 + 8u * (2 * NARROW_MAX_STAGES);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * NARROW_MAX_STAGES + 1));
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 8 * (2 * NARROW_MAX_STAGES + 1) + 4);
+    auto CFULL = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(2 * NARROW_MAX_STAGES + 1 + b); };
+    auto CEMPTY = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(2 * NARROW_MAX_STAGES + 3 + b); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * NARROW_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 8 * NARROW_BARS + 4);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = static_cast<int>(gridDim.x) / ((p.N + ROWS - 1) / ROWS);   // the cluster's blocks
@@ -306,7 +457,7 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS)
     const int nk_all = (p.K + BK - 1) / BK;
     const int k_first = static_cast<int>(static_cast<long long>(nk_all) * rank / split);
     const int nk = static_cast<int>(static_cast<long long>(nk_all) * (rank + 1) / split) - k_first;
-    const uint32_t ncols = narrow_cols(p.tt);
+    const uint32_t cols = static_cast<uint32_t>(narrow_cols(p.tt)), ncols = ACC != 0 ? 2 * cols : cols;
 
     if (tid == 0) {
         tma_prefetch_map(&w_map);
@@ -316,6 +467,10 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS)
             mbar_init(EMPTY(s), 1);
         }
         mbar_init(DONE, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(CFULL(b), 1);
+            mbar_init(CEMPTY(b), 8);
+        }
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -351,6 +506,11 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS)
         const uint32_t id = idesc(p, ROWS, p.tt);
         for (int kc = 0; kc < nk; ++kc) {
             const int s = kc % NSTG;
+            const int chain = ACC != 0 ? kc / SEG : 0, first = chain * SEG, b = chain & 1;
+            if (ACC != 0 && kc == first && chain >= 2) {   // the accumulator of two chains ago has been added up
+                const bool free = wait_bounded(CEMPTY(b), (chain / 2 - 1) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, free)) break;
+            }
             const bool got = wait_bounded(FULL(s), (kc / NSTG) & 1, abort_flag);
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
@@ -359,24 +519,54 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS)
                                     smem_desc_sw128(wa + 96)};
             const uint64_t bd[4] = {smem_desc_sw128(xa), smem_desc_sw128(xa + 32), smem_desc_sw128(xa + 64),
                                     smem_desc_sw128(xa + 96)};
-            tc_mma_ss4(tmem, ad, bd, id, kc > 0 ? 1u : 0u);
+            tc_mma_ss4(tmem + b * cols, ad, bd, id, kc > first ? 1u : 0u);
             tc_commit(EMPTY(s));
+            if (ACC != 0 && (kc == first + SEG - 1 || kc == nk - 1)) tc_commit(CFULL(b));
         }
         tc_commit(DONE);
+    }
+    // ---- promotion: warp w >= 2 adds up 32 rows of the chains' accumulators, of
+    // one half of the columns (all of them, if there are 32) ----
+    const int quad = warp & 3, half = ACC != 0 ? (warp - 2) >> 2 : warp >> 2;
+    const uint32_t row = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+    float acc[ACC != 0 ? ACC : 1];
+    if (ACC != 0 && warp >= 2) {
+#pragma unroll
+        for (int j = 0; j < ACC; ++j) acc[j] = 0.f;
+        const int chains = (nk + SEG - 1) / SEG;
+        for (int c = 0; c < chains; ++c) {
+            const bool got = wait_bounded(CFULL(c & 1), (c / 2) & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < ACC / 32; ++q) {
+                const uint32_t c0 = static_cast<uint32_t>(half * ACC + 32 * q);
+                if (c0 >= cols) continue;
+                uint32_t v[32];
+                tc_ld32(row + (c & 1) * cols + c0, v);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[32 * q + j] += __uint_as_float(v[j]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(CEMPTY(c & 1));
+        }
     }
     const bool done = wait_bounded(DONE, 0, abort_flag, false, TEARDOWN_LIMIT_NS);
     tc_fence_after();
     __syncthreads();   // the loads have landed (warp 0) and the MMAs are done: the ring is free
 
-    // ---- partial sums to shared memory: red[t][n], lane = weight row; a warp
-    // reads the 32 rows that its number allows, every other 32 tokens ----
+    // ---- partial sums to shared memory: red[t][n], lane = weight row ----
     const int tn = p.T - t0 < p.tt ? p.T - t0 : p.tt;      // the tile's tokens
     float* red = reinterpret_cast<float*>(smem);
-    if (__all_sync(0xffffffffu, done && !*abort_flag)) {
-        const int quad = warp & 3;
-        const uint32_t row = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+    if (ACC != 0) {
+#pragma unroll
+        for (int j = 0; j < ACC; ++j)
+            if (warp >= 2 && half * ACC + j < tn) red[(half * ACC + j) * RED_PITCH + 32 * quad + lane] = acc[j];
+    } else if (__all_sync(0xffffffffu, done && !*abort_flag)) {
         uint32_t v[32];
-        for (int c0 = 32 * (warp >> 2); c0 < tn; c0 += 64) {
+        for (int c0 = 32 * half; c0 < tn; c0 += 64) {
             tc_ld32(row + static_cast<uint32_t>(c0), v);
             tc_wait_ld();
 #pragma unroll
@@ -389,10 +579,10 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS)
 
     // ---- this block's share of the tile: sum over the cluster, epilogue ----
     switch (split) {
-        case 1: narrow_finish<1>(p, ring, rank, n0, t0, tn); break;
-        case 2: narrow_finish<2>(p, ring, rank, n0, t0, tn); break;
-        case 4: narrow_finish<4>(p, ring, rank, n0, t0, tn); break;
-        default: narrow_finish<8>(p, ring, rank, n0, t0, tn); break;
+        case 1: narrow_finish<1, NARROW_THREADS<ACC>>(p, ring, rank, n0, t0, tn); break;
+        case 2: narrow_finish<2, NARROW_THREADS<ACC>>(p, ring, rank, n0, t0, tn); break;
+        case 4: narrow_finish<4, NARROW_THREADS<ACC>>(p, ring, rank, n0, t0, tn); break;
+        default: narrow_finish<8, NARROW_THREADS<ACC>>(p, ring, rank, n0, t0, tn); break;
     }
     cluster_sync();   // the other blocks have read this one's sums
     if (warp == 1) {
@@ -402,35 +592,87 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS)
     if (tid == 0 && *abort_flag) atomicOr(p.err, STATUS_LINEAR_WAIT);
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::WIDE_THREADS, 1)
+namespace lin {
+// SPLIT: the block's share (128 / S tokens) of its half of a tile.
+template <int S, int BN>
+__device__ __forceinline__ void wide_finish(const Params& p, uint32_t part, uint32_t cluster_rank, long long t0, int n0) {
+    constexpr int PITCH = Wide<BN, true, false>::PART_PITCH, U = 2;
+    const uint32_t half = cluster_rank & 1;
+    const int row0 = static_cast<int>(cluster_rank >> 1) * (ROWS / S);
+    uint32_t base[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) base[s] = in_block(part, 2 * s + half);
+    constexpr int ITEMS = ROWS / S * (BN / 4);
+    for (int ii = threadIdx.x; ii < ITEMS; ii += U * WIDE_THREADS) {
+        float4 q[U][S];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = ii + u * WIDE_THREADS;
+            if (i >= ITEMS) continue;
+            const uint32_t at = static_cast<uint32_t>((row0 + i / (BN / 4)) * PITCH + i % (BN / 4) * 4) * 4u;
+#pragma unroll
+            for (int s = 0; s < S; ++s) q[u][s] = ld_cluster_f4(base[s] + at);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = ii + u * WIDE_THREADS;
+            const long long t = t0 + row0 + i / (BN / 4);
+            const int n = n0 + i % (BN / 4) * 4;
+            if (i >= ITEMS || t >= p.T || n >= p.N) continue;
+            float v[4] = {q[u][0].x, q[u][0].y, q[u][0].z, q[u][0].w};
+#pragma unroll
+            for (int s = 1; s < S; ++s) {
+                v[0] += q[u][s].x; v[1] += q[u][s].y; v[2] += q[u][s].z; v[3] += q[u][s].w;
+            }
+            if (p.bias != nullptr) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < p.N) v[e] += load16(p.bias, n + e, p.fp16);
+            }
+            activate(v, p.act);
+            store4(p, t, n, v);
+        }
+    }
+}
+}  // namespace lin
+
+template <int BN, bool SPLIT, bool PROMOTE>
+__global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
     linear_wide_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
                        const lin::Params p) {
     using namespace lin;
+    using C = Wide<BN, SPLIT, PROMOTE>;
+    constexpr int STAGES = C::STAGES, STAGE = C::STAGE, COLS = BN * C::BUFS;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    const uint32_t ring = smem_addr(smem);                 // [stage][128 tokens | 128 weight rows]
-    float* epi = reinterpret_cast<float*>(smem + WIDE_STAGES * WIDE_STAGE);
-    uint8_t* ctrl = smem + WIDE_STAGES * WIDE_STAGE + WIDE_EPI;
+    const uint32_t ring = smem_addr(smem);                 // [stage][128 tokens | BN / 2 weight rows]
+    float* epi = reinterpret_cast<float*>(smem + STAGES * STAGE);
+    uint8_t* ctrl = smem + STAGES * STAGE + C::EPI;
     const uint32_t bar0 = smem_addr(ctrl);
     auto FULL = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(s); };
-    auto EMPTY = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(WIDE_STAGES + s); };
-    auto TFULL = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(2 * WIDE_STAGES + b); };
-    auto TEMPTY = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(2 * WIDE_STAGES + 2 + b); };
-    const uint32_t DONE = bar0 + 8u * (2 * WIDE_STAGES + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * WIDE_BARS);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 8 * WIDE_BARS + 4);
+    auto EMPTY = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(STAGES + s); };
+    auto TFULL = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(2 * STAGES + b); };
+    auto TEMPTY = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(2 * STAGES + 2 + b); };
+    const uint32_t DONE = bar0 + 8u * (2 * STAGES + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * C::BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 8 * C::BARS + 4);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = static_cast<int>(cluster_rank());
-    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const uint32_t crank = cluster_rank(), leader = crank & ~1u;   // the pair's first block
+    const int rank = static_cast<int>(crank & 1);
     const int tiles = p.mt * p.nt;
-    const int nk = (p.K + BK - 1) / BK;
+    // the pair's tiles and its part of their K range
+    const int split = SPLIT ? p.split : 1;
+    const int pair = blockIdx.x / (2 * split), pairs = SPLIT ? tiles : gridDim.x / 2;
+    const int nk_all = (p.K + BK - 1) / BK, part = SPLIT ? static_cast<int>(crank >> 1) : 0;
+    const int k_first = static_cast<int>(static_cast<long long>(nk_all) * part / split);
+    const int nk = static_cast<int>(static_cast<long long>(nk_all) * (part + 1) / split) - k_first;
 
     if (tid == 0) {
         tma_prefetch_map(&w_map);
         tma_prefetch_map(&x_map);
-        for (int s = 0; s < WIDE_STAGES; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(FULL(s), 1);    // used in the pair's first block: its expected bytes are both blocks'
             mbar_init(EMPTY(s), 1);
         }
@@ -443,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::WIDE_THREADS, 1
         mbar_fence_init();
     }
     if (warp == 2) {
-        tc2_alloc(smem_addr(tmem_slot), 512);
+        tc2_alloc(smem_addr(tmem_slot), COLS);
         tc2_relinquish();
     }
     tc_fence_before();
@@ -470,79 +712,123 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::WIDE_THREADS, 1
             for (int tile = pair; tile < tiles && ok; tile += pairs) {
                 int m, n;
                 place(tile, &m, &n);
-                const int y = m * 256 + rank * ROWS, z = n * 256 + rank * ROWS;
+                const int y = m * 256 + rank * ROWS, z = n * BN + rank * (BN / 2);
                 for (int kc = 0; kc < nk; ++kc, ++it) {
-                    const int s = it % WIDE_STAGES;
-                    if (it >= WIDE_STAGES && !wait_bounded(EMPTY(s), (it / WIDE_STAGES - 1) & 1, abort_flag)) {
+                    const int s = it % STAGES;
+                    if (it >= STAGES && !wait_bounded(EMPTY(s), (it / STAGES - 1) & 1, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(FULL(s), 2 * WIDE_STAGE);
-                    const uint32_t full = in_block(FULL(s), 0);
-                    tma2_load_2d(ring + s * WIDE_STAGE, &x_map, kc * BK, y, full);
-                    tma2_load_2d(ring + s * WIDE_STAGE + TILE, &w_map, kc * BK, z, full);
+                    if (rank == 0) mbar_arrive_expect_tx(FULL(s), 2 * STAGE);
+                    const uint32_t full = in_block(FULL(s), leader);
+                    tma2_load_2d(ring + s * STAGE, &x_map, (k_first + kc) * BK, y, full);
+                    tma2_load_2d(ring + s * STAGE + TILE, &w_map, (k_first + kc) * BK, z, full);
                 }
             }
             // the loads in flight land before the pair leaves (on the first block's barriers)
             if (rank == 0)
-                for (int i = it > WIDE_STAGES ? it - WIDE_STAGES : 0; i < it; ++i)
-                    wait_bounded(FULL(i % WIDE_STAGES), (i / WIDE_STAGES) & 1, abort_flag, false, TEARDOWN_LIMIT_NS);
+                for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
+                    wait_bounded(FULL(i % STAGES), (i / STAGES) & 1, abort_flag, false, TEARDOWN_LIMIT_NS);
         }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
-            const uint32_t id = idesc(p, 256, 256);
+            const uint32_t id = idesc(p, 256, BN);
             int it = 0, local = 0;
             bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += pairs, ++local) {
-                const int b = local & 1;
-                if (local >= 2) {
-                    const bool got = wait_bounded(TEMPTY(b), (local / 2 - 1) & 1, abort_flag);
-                    ok = __all_sync(0xffffffffu, got);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
+            // `local` counts the accumulators handed to the epilogue: one a tile, or
+            // with PROMOTE one a chain
+            for (int tile = pair; tile < tiles && ok; tile += pairs) {
                 for (int kc = 0; kc < nk; ++kc, ++it) {
-                    const int s = it % WIDE_STAGES;
-                    const bool got = wait_bounded(FULL(s), (it / WIDE_STAGES) & 1, abort_flag);
+                    const int s = it % STAGES, b = local & 1;
+                    const bool first = PROMOTE ? kc % SEG == 0 : kc == 0;
+                    if (first && local >= 2) {
+                        const bool got = wait_bounded(TEMPTY(b), (local / 2 - 1) & 1, abort_flag);
+                        ok = __all_sync(0xffffffffu, got);
+                        if (!ok) break;
+                    }
+                    const bool got = wait_bounded(FULL(s), (it / STAGES) & 1, abort_flag);
                     ok = __all_sync(0xffffffffu, got);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = ring + s * WIDE_STAGE;
-                    tc2_mma_ss4(tmem + 256u * b, smem_desc_sw128(a), smem_desc_sw128(a + TILE), id, kc > 0 ? 1u : 0u);
-                    tc2_commit_both(EMPTY(s));
+                    const uint32_t a = ring + s * STAGE;
+                    tc2_mma_ss4(tmem + static_cast<uint32_t>(BN * b), smem_desc_sw128(a), smem_desc_sw128(a + TILE), id,
+                                first ? 0u : 1u);
+                    tc2_commit_both(EMPTY(s), leader);
+                    if (kc == nk - 1 || (PROMOTE && kc % SEG == SEG - 1)) {
+                        tc2_commit_both(TFULL(b), leader);
+                        ++local;
+                    }
                 }
-                if (ok) tc2_commit_both(TFULL(b));
             }
-            tc2_commit_both(DONE);
+            tc2_commit_both(DONE, leader);
         }
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
         float* mine = epi + (warp - 4) * 32 * WIDE_PITCH;
         int local = 0;
-        for (int tile = pair; tile < tiles; tile += pairs, ++local) {
-            const int b = local & 1;
-            const bool got = wait_bounded(TFULL(b), (local / 2) & 1, abort_flag);
-            if (!__all_sync(0xffffffffu, got)) break;
-            tc_fence_after();
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            float acc[PROMOTE ? BN / 2 : 1];
+            const int chains = PROMOTE ? (nk + SEG - 1) / SEG : 1;
+            if (PROMOTE) {
+#pragma unroll
+                for (int j = 0; j < BN / 2; ++j) acc[j] = 0.f;
+            }
+            uint32_t src = 0;
+            auto release = [&](int b) {   // the accumulator has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(in_block(TEMPTY(b), leader));
+            };
+            int b = 0;
+            for (int c = 0; c < chains; ++c, ++local) {
+                b = local & 1;
+                const bool got = wait_bounded(TFULL(b), (local / 2) & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
+                tc_fence_after();
+                src = tmem + static_cast<uint32_t>(BN * b + BN / 2 * half) + (static_cast<uint32_t>(32 * quad) << 16);
+                if (PROMOTE) {
+#pragma unroll
+                    for (int q = 0; q < BN / 64; ++q) {
+                        uint32_t raw[32];
+                        tc_ld32(src + 32u * q, raw);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[32 * q + j] += __uint_as_float(raw[j]);
+                    }
+                    release(b);
+                }
+            }
+            if (!ok) break;
             int m, n;
             place(tile, &m, &n);
             const long long row0 = static_cast<long long>(m) * 256 + rank * ROWS + quad * 32;
-            const uint32_t src = tmem + 256u * b + 128u * half + (static_cast<uint32_t>(32 * quad) << 16);
-            for (int c = 0; c < 4; ++c) {   // 32 columns at a time
-                const int col0 = n * 256 + half * 128 + c * 32;
-                uint32_t raw[32];
-                tc_ld32(src + 32u * c, raw);
-                tc_wait_ld();
-                if (c == 3) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(in_block(TEMPTY(b), 0));
-                }
-                if (col0 >= p.N) continue;
-                float v[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+            for (int c = 0; c < BN / 64; ++c) {   // 32 columns at a time
+                const int col0 = n * BN + half * (BN / 2) + c * 32;
+                float v[32];
+                if (PROMOTE) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = acc[32 * (PROMOTE ? c : 0) + j];
+                } else {
+                    uint32_t raw[32];
+                    tc_ld32(src + 32u * c, raw);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                }
+                if (SPLIT) {
+                    // the partial sums take the ring's place: its pair's MMAs are done
+                    float* to = reinterpret_cast<float*>(smem) + (quad * 32 + lane) * C::PART_PITCH + half * (BN / 2) + c * 32;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<float4*>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    continue;
+                }
+                if (!PROMOTE && c == BN / 64 - 1) release(b);
+                if (col0 >= p.N) continue;
                 if (p.bias != nullptr) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] += col0 + j < p.N ? load16(p.bias, col0 + j, p.fp16) : 0.f;
@@ -555,13 +841,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::WIDE_THREADS, 1
                     *reinterpret_cast<float4*>(mine + lane * WIDE_PITCH + j) =
                         make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                 __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = i * 4 + (lane >> 3), j = (lane & 7) * 4;
-                    const float4 q = *reinterpret_cast<const float4*>(mine + r * WIDE_PITCH + j);
-                    const float o[4] = {q.x, q.y, q.z, q.w};
-                    if (row0 + r < p.T && col0 + j < p.N) store4(p, row0 + r, col0 + j, o);
-                }
+                if (p.out == OUT_F32) write32<OUT_F32>(p, mine, row0, col0, lane);
+                else if (p.out == OUT_BF16) write32<OUT_BF16>(p, mine, row0, col0, lane);
+                else write32<OUT_F16>(p, mine, row0, col0, lane);
             }
         }
     }
@@ -570,9 +852,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::WIDE_THREADS, 1
     tc_fence_before();
     __syncthreads();
     cluster_sync();
+    if (SPLIT) {   // the partial sums of all pairs are there
+        int m, n;
+        place(pair, &m, &n);
+        const long long t0 = static_cast<long long>(m) * 256 + rank * ROWS;
+        if (split == 2) wide_finish<2, BN>(p, ring, crank, t0, n * BN);
+        else wide_finish<4, BN>(p, ring, crank, t0, n * BN);
+        cluster_sync();   // and have been read
+    }
     if (warp == 2) {
         tc_fence_after();
-        tc2_dealloc(tmem, 512);
+        tc2_dealloc(tmem, COLS);
     }
     if (tid == 0 && *abort_flag) atomicOr(p.err, STATUS_LINEAR_WAIT);
 }

@@ -142,11 +142,12 @@ __device__ __forceinline__ uint32_t index_of(uint64_t c) { return 0xffffffffu - 
 
 // A value that at least K of the threads' keys reach, and as far as their bits
 // tell them apart no more than K + K / 4 + 2: bisection over the key's bits, a
-// counting barrier a bit (about 12 of them; taking maxima out one by one costs
-// 200 cycles each).  All threads call it; its first barrier also covers what
-// they wrote before.
+// counting barrier a bit (about 12 of them, 200 cycles each; one warp alone
+// took 300 a bit, taking maxima out one by one 200 for each of the K).  All
+// threads call it; its first barrier also covers what they wrote before.
 __device__ __forceinline__ uint32_t kth_key(uint32_t key, int K) {
     uint32_t t = 0;
+#pragma unroll 1
     for (int bit = 31; bit >= 0; --bit) {
         const uint32_t up = t | 1u << bit;
         const int c = __syncthreads_count(key >= up);
@@ -177,7 +178,7 @@ struct BeamParams {
 // How many of n candidates are better.
 __device__ __forceinline__ int beam_rank(const uint64_t* c, int n, uint64_t mine) {
     int rank = 0;
-#pragma unroll 8
+#pragma unroll 2
     for (int j = 0; j < n; ++j) rank += c[j] > mine;
     return rank;
 }
@@ -303,40 +304,45 @@ __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamPa
     // ---- the K best: the warp reads the elements of each thread that reaches
     // the threshold again, a vector a lane ----
     uint32_t pass = __ballot_sync(0xffffffffu, m > NEG_INF && m >= thr);
+#pragma unroll 1
     while (pass != 0) {
-        // two threads' vectors at a time
+        // two threads' vectors at a time; which elements pass as bits, so that the
+        // code that few elements reach is small (it is fetched when it is needed)
         const int from = tid - lane + __ffs(pass) - 1;
         pass &= pass - 1;
         const int other = pass != 0 ? tid - lane + __ffs(pass) - 1 : -1;
         pass &= pass - 1;
+#pragma unroll 1
         for (int i = lane; i < p.NV; i += 32) {
-            const int v[2] = {at(i, from), other >= 0 ? at(i, other) : p.V};
+            const int v0 = at(i, from), v1 = other >= 0 ? at(i, other) : p.V;
             uint32_t w[2][4];
-            beam_load<T>(w[0], x, v[0], p.V, mis);
-            beam_load<T>(w[1], x, v[1], p.V, mis);
+            beam_load<T>(w[0], x, v0, p.V, mis);
+            beam_load<T>(w[1], x, v1, p.V, mis);
+            uint32_t bits = 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int q = 0; q < VEC / 2; ++q) {
-                    const float2 e = E::pair(w[h], q);
-                    if (e.x >= thr && e.x > NEG_INF) {
-                        const int k = atomicAdd(&s_n, 1);
-                        if (k < BUF) s_c[k] = pack(e.x, v[h] + 2 * q);
-                    }
-                    if (e.y >= thr && e.y > NEG_INF) {
-                        const int k = atomicAdd(&s_n, 1);
-                        if (k < BUF) s_c[k] = pack(e.y, v[h] + 2 * q + 1);
-                    }
+            for (int q = 0; q < VEC; ++q) {
+                const float2 e = E::pair(w[q / (VEC / 2)], q % (VEC / 2));
+                bits |= (e.x >= thr ? 1u : 0u) << 2 * q | (e.y >= thr ? 2u : 0u) << 2 * q;
+            }
+#pragma unroll 1
+            for (; bits != 0; bits &= bits - 1) {
+                const int u = __ffs(bits) - 1, v = u < VEC ? v0 + u : v1 + u - VEC;
+                // past the row's end (or masked) there is nothing, whatever the threshold
+                const float e = v < p.V ? E::one(reinterpret_cast<const uint8_t*>(x + v)) : NEG_INF;
+                if (e > NEG_INF) {
+                    const int k = atomicAdd(&s_n, 1);
+                    if (k < BUF) s_c[k] = pack(e, v);
                 }
+            }
         }
     }
     __syncthreads();
     const size_t part = static_cast<size_t>(row) * p.S + blockIdx.x;
-    if (tid == 0) {
-        total = 0;
+    if (tid >= THREADS - 32) {   // the last warp, which has no candidate to rank
+        total = lane < THREADS / 32 ? s_sum[lane] : 0.0;
 #pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) total += s_sum[w];
-        p.sums[part] = make_float2(top, static_cast<float>(total));
+        for (int d = THREADS / 64; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+        if (lane == 0) p.sums[part] = make_float2(top, static_cast<float>(total));
     }
     uint64_t* out = p.cand + part * p.K;
     const int n = s_n;
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
             const double key = s_score[i];
             const int flat = s_flat[i];
             int rank = 0;
-#pragma unroll 8
+#pragma unroll 2
             for (int j = 0; j < n; ++j) {
                 const double other = s_score[j];
                 rank += (other > key) | ((other == key) & (s_flat[j] < flat));

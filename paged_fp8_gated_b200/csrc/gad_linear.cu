@@ -7,7 +7,6 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <mutex>
 
 #include "gad_host.h"
 #include "gad_linear.cuh"
@@ -129,30 +128,37 @@ int capacity_of(OncePerContext& once, int smem, int cluster, int* out) {
 
 OncePerContext g_narrow_smem[4], g_wide_smem[8];
 
-// Asked once per (device, context).
-int capacity(const Capacity** out) {
+// Asked once per (device, context); two threads that ask at the same time store
+// the same answers.
+int capacity(Capacity* out) {
     static OncePerContext asked, raised;
-    static Capacity cap[kMaxDevices];
-    static std::mutex lock;
+    static std::atomic<int> known[kMaxDevices][kClasses * kSplits + 3];
     int dev = 0;
     const int ds = current_device(&dev);
     if (ds != GAD_OK) return ds;
-    *out = &cap[dev];
-    if (asked.is_done(dev, current_ctx_id())) return GAD_OK;
-    const std::lock_guard<std::mutex> hold(lock);
-    if (asked.is_done(dev, current_ctx_id())) return GAD_OK;
-    Capacity c;
+    const bool ask = !asked.is_done(dev, current_ctx_id());
+    int i = 0;
+    auto get = [&](int smem, int cluster, int* n) {
+        if (ask) {
+            const int st = capacity_of(raised, smem, cluster, n);
+            if (st != GAD_OK) return st;
+            known[dev][i].store(*n, std::memory_order_release);
+        } else {
+            *n = known[dev][i].load(std::memory_order_acquire);
+        }
+        ++i;
+        return static_cast<int>(GAD_OK);
+    };
     for (int m = 0; m < kClasses; ++m)
         for (int k = 0; k < kSplits; ++k) {
-            const int st = capacity_of(raised, smem_share(512 >> m), 1 << k, &c.narrow[m][k]);
+            const int st = get(smem_share(512 >> m), 1 << k, &out->narrow[m][k]);
             if (st != GAD_OK) return st;
         }
     for (int k = 0; k < 3; ++k) {
-        const int st = capacity_of(raised, smem_share(512), 2 << k, &c.wide[k]);
+        const int st = get(smem_share(512), 2 << k, &out->wide[k]);
         if (st != GAD_OK) return st;
     }
-    cap[dev] = c;
-    asked.mark(dev);
+    if (ask) asked.mark(dev);
     return GAD_OK;
 }
 
@@ -170,15 +176,15 @@ constexpr int kLongChain = 768 / gad::lin::BK;
 // from 256 x 32,000 to 8,192 x 32,001, cold weights:
 //   narrow: a stage takes a block 0.30 (an SM draws 54 GB/s of weights), or its
 //     bytes at an SM's 123 GB/s from L2, or all blocks' weights at 6.4 TB/s, or
-//     a load's latency (2.0) over the stages in flight; a
-//     block's fixed part is its cluster's start, its share of the epilogue and
-//     the exchange with the cluster.  Example (cold weights): 32 x
-//     8,192 x 2,304 (18 tiles) 42 / 23 / 14 / 12 in clusters of 1 / 2 / 4 / 8.
+//     a load's latency (2.0) over the stages in flight; a block's fixed part is
+//     its cluster's start, its share of the epilogue and the exchange with the
+//     cluster.  Example: 32 x 8,192 x 2,304 (18 tiles) 42 / 23 / 14 / 12 in
+//     clusters of 1 / 2 / 4 / 8 blocks.
 //   wide: a stage of 256 x 256 takes a pair 0.33 (the tensor cores' time; 0.41
-//     when no other tile reads the same weights), one of 256 x 128 0.25 (an SM's
-//     share of L2 bandwidth).  Example: 768 x 8,192 x
-//     2,304 44 on 27 of 74 pairs, 29 with two pairs a tile; 1,024 x 8,192 x 2,304
-//     (36 tiles, more than the 33 clusters of four blocks that fit) 44 and 55.
+//     when no other tile reads the same weights), one of 256 x 128 0.265 (an SM's
+//     share of L2 bandwidth).  Example: 768 x 8,192 x 2,304 44 on 27 of 74 pairs,
+//     29 with two pairs a tile; 1,024 x 8,192 x 2,304 (36 tiles, more than the 33
+//     clusters of four blocks that fit) 44 and 55.
 Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
     using namespace gad::lin;
     const int nk = (K + BK - 1) / BK;
@@ -232,7 +238,7 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
             q.promote = promote;
             const double waves = std::ceil(tiles / cap.wide[k]);
             if (k == 0)
-                q.us = bn == 256 ? 6.7 + waves * std::fmax(own * stage256, 3.0) : 5.0 + waves * std::fmax(own * 0.25, 1.9);
+                q.us = bn == 256 ? 6.7 + waves * std::fmax(own * stage256, 3.0) : 5.0 + waves * std::fmax(own * 0.265, 1.9);
             else
                 q.us = 3.5 + waves * (bn == 256 ? own * stage256 + 5.3 : own * 0.22 + 2.5);
             q.us = std::fmax(q.us, 3.5 + dram);
@@ -367,10 +373,10 @@ int gad_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const voi
     st = linear_status_word(&p.err);
     if (st != GAD_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Capacity* cap = nullptr;
+    Capacity cap;
     st = capacity(&cap);
     if (st != GAD_OK) return st;
-    const Plan plan = choose(T, K, N, out_dtype == GAD_DTYPE_F32, *cap, sms);
+    const Plan plan = choose(T, K, N, out_dtype == GAD_DTYPE_F32, cap, sms);
     if (plan.kind == Plan::WIDE)
         return plan.promote ? launch_wide<true>(p, x, ldx, w, ldw, plan, sms, s)
                             : launch_wide<false>(p, x, ldx, w, ldw, plan, sms, s);

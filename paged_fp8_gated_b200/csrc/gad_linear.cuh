@@ -239,6 +239,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
 }
 
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
+}
+// Counts `bytes` as arrived on a barrier of this block.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // ---- tcgen05 on a pair of blocks (cta_group::2) ----
 __device__ __forceinline__ void tc2_alloc(uint32_t dst_smem, uint32_t ncols) {  // whole warp, in both blocks
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(dst_smem), "r"(ncols)
@@ -321,7 +329,7 @@ struct Wide {
     static constexpr int EPI = WIDE_EPI_WARPS * 32 * WIDE_PITCH * 4;
     static constexpr int BUFS = SPLIT && !PROMOTE ? 1 : 2;  // accumulators
     static constexpr int BARS = 2 * STAGES + 5;           // full, empty, 2 tile full, 2 tile empty, done
-    static constexpr int SMEM = 1024 + STAGES * STAGE + EPI + 8 * BARS + 8;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + EPI + 8 * BARS + 16;
     static constexpr int PART_PITCH = BN + 4;             // SPLIT: floats per token of the partial sums
     static_assert(!SPLIT || ROWS * PART_PITCH * 4 <= STAGES * STAGE, "the partial sums fit the ring");
     static_assert(!PROMOTE || BN == 128, "64 sums a thread");
@@ -657,6 +665,9 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
     const uint32_t DONE = bar0 + 8u * (2 * STAGES + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * C::BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 8 * C::BARS + 4);
+    // stages that this block has asked for, and (bit 31: it gave up) the other one
+    uint32_t* own_end = reinterpret_cast<uint32_t*>(ctrl + 8 * C::BARS + 8);
+    uint32_t* other_end = own_end + 1;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t crank = cluster_rank(), leader = crank & ~1u;   // the pair's first block
@@ -725,10 +736,7 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
                     tma2_load_2d(ring + s * STAGE + TILE, &w_map, (k_first + kc) * BK, z, full);
                 }
             }
-            // the loads in flight land before the pair leaves (on the first block's barriers)
-            if (rank == 0)
-                for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
-                    wait_bounded(FULL(i % STAGES), (i / STAGES) & 1, abort_flag, false, TEARDOWN_LIMIT_NS);
+            *own_end = static_cast<uint32_t>(it);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -851,7 +859,27 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
     wait_bounded(DONE, 0, abort_flag, false, TEARDOWN_LIMIT_NS);
     tc_fence_before();
     __syncthreads();
+    if (tid == 0) {
+        if (*abort_flag) *own_end |= 0x80000000u;
+        st_cluster_u32(in_block(smem_addr(other_end), crank ^ 1u), *own_end);
+    }
     cluster_sync();
+    // All loads were used, so have landed, unless a block gave up.  Then the pair's
+    // first block waits for the ones in flight, on its barriers: for a stage that
+    // only one block has asked for, it makes up what the barrier still expects.
+    if (*own_end != *other_end || (*own_end >> 31) != 0) {
+        if (rank == 0 && tid == 0) {
+            const int mine = static_cast<int>(*own_end & 0x7fffffffu), theirs = static_cast<int>(*other_end & 0x7fffffffu);
+            const int last = mine > theirs ? mine : theirs;
+            for (int i = last > STAGES ? last - STAGES : 0; i < last; ++i) {
+                if (i >= theirs) mbar_complete_tx(FULL(i % STAGES), STAGE);
+                else if (i >= mine) mbar_arrive_expect_tx(FULL(i % STAGES), STAGE);
+                wait_bounded(FULL(i % STAGES), (i / STAGES) & 1, abort_flag, false, TEARDOWN_LIMIT_NS);
+            }
+        }
+        __syncthreads();
+        cluster_sync();
+    }
     if (SPLIT) {   // the partial sums of all pairs are there
         int m, n;
         place(pair, &m, &n);

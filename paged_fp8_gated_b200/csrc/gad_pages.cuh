@@ -245,18 +245,22 @@ struct ForkParams {
 template <int U, bool VEC>
 __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
     using namespace pg;
-    __shared__ int s_kids[ROWS], s_elder[ROWS], s_par[ROWS], s_len[ROWS], s_new[ROWS];
-    static_assert(!VEC || U == 4, "a vector is four entries");
+    __shared__ int s_kids[ROWS], s_elder[ROWS], s_par[ROWS];
+    // what is to be known of an old row: entries to look at (none, if its one child
+    // takes them all), the partly filled last one, the changes of the counts; of a
+    // new one: entries that it takes over
+    __shared__ int s_n[ROWS], s_last[ROWS], s_take[ROWS];
     const int y0 = blockIdx.y * ROWS, tid = threadIdx.x;
     pdl_launch_dependents();
+    int len = -1, new_len = -1;
     if (tid < ROWS) {
         const int y = y0 + tid;
         int par = y < p.rows_out ? p.parent[y] : -1;
         if (par >= p.rows_in) par = -1;
         s_kids[tid] = s_elder[tid] = 0;
         s_par[tid] = par;
-        s_len[tid] = y < p.rows_in ? p.lens[y] : -1;
-        s_new[tid] = par >= 0 ? p.lens[par] : -1;
+        len = y < p.rows_in ? p.lens[y] : -1;
+        new_len = par >= 0 ? p.lens[par] : -1;
     }
     __syncthreads();
     for (int r = tid; r < p.rows_out; r += THREADS) {
@@ -267,10 +271,26 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
             if (r < y0 + k && q == s_par[k]) s_elder[k] = 1;
     }
     __syncthreads();
+    if (tid < ROWS) {
+        const int n = pages_of(len, p.shift, p.max_pages);
+        s_n[tid] = s_kids[tid] == 1 ? 0 : n;
+        s_last[tid] = has_partial(len, p.shift, p.max_pages) ? n - 1 : -1;
+        const bool fresh = s_elder[tid] && has_partial(new_len, p.shift, p.max_pages);
+        s_take[tid] = pages_of(new_len, p.shift, p.max_pages) - fresh;
+        const int y = y0 + tid;
+        if (blockIdx.x == 0 && y < p.rows_out) {
+            p.out_lens[y] = new_len < 0 ? -1 : new_len;
+            p.copy_src[y] = -1;
+            p.copy_dst[y] = -1;
+            p.ws.rows[y] = fresh;
+            if (y == 0) p.ws.head->status = 0;
+        }
+    }
+    __syncthreads();
 
     const int c0 = blockIdx.x * (U * THREADS);
     auto col = [&](int u) { return VEC ? c0 + U * tid + u : c0 + u * THREADS + tid; };
-    // the four entries of a row (any value from `n` on)
+    // the entries of a row (any value from `n` on)
     auto entries = [&](int (&e)[U], const int* row, int n) {
         if (VEC) {
             const int4 q = col(0) < n ? *reinterpret_cast<const int4*>(row + col(0)) : make_int4(-1, -1, -1, -1);
@@ -281,27 +301,24 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
         }
     };
     int e[ROWS][U];   // all rows' entries at a time
+    const int* old = p.table + static_cast<size_t>(y0) * p.max_pages;
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-        const int n = s_kids[k] == 1 ? 0 : pages_of(s_len[k], p.shift, p.max_pages);
-        entries(e[k], p.table + static_cast<size_t>(y0 + k) * p.max_pages, n);
-    }
+    for (int k = 0; k < ROWS; ++k, old += p.max_pages) entries(e[k], old, s_n[k]);
     int page[U], left[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) page[u] = -1, left[u] = 0;
     auto flush = [&](int u) {
-        if (left[u] != 0 && page[u] >= 0 && page[u] < p.pool.num_pages) atomicAdd(p.pool.refs + page[u], left[u]);
+        if (left[u] != 0 && static_cast<unsigned>(page[u]) < static_cast<unsigned>(p.pool.num_pages))
+            atomicAdd(p.pool.refs + page[u], left[u]);
     };
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
-        const int kids = s_kids[k], len = s_len[k];
-        const int n = kids == 1 ? 0 : pages_of(len, p.shift, p.max_pages);
-        const int last = has_partial(len, p.shift, p.max_pages) ? n - 1 : -1;
+        const int n = s_n[k], last = s_last[k], kids = s_kids[k];
+        if (n <= c0) continue;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (col(u) >= n) continue;
-            const int d = (col(u) == last ? min(kids, 1) : kids) - 1;
-            if (e[k][u] != page[u]) {
+            const int d = col(u) >= n ? 0 : (col(u) == last ? min(kids, 1) : kids) - 1;
+            if (d != 0 && e[k][u] != page[u]) {
                 flush(u);
                 page[u] = e[k][u];
                 left[u] = 0;
@@ -312,32 +329,20 @@ __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) flush(u);
 
-    auto taken = [&](int k) {   // entries that new row y0 + k takes over
-        const bool fresh = s_elder[k] && has_partial(s_new[k], p.shift, p.max_pages);
-        return pages_of(s_new[k], p.shift, p.max_pages) - fresh;
-    };
 #pragma unroll
     for (int k = 0; k < ROWS; ++k)
-        entries(e[k], p.table + static_cast<size_t>(s_par[k] >= 0 ? s_par[k] : 0) * p.max_pages, taken(k));
+        entries(e[k], p.table + static_cast<size_t>(max(s_par[k], 0)) * p.max_pages, s_take[k]);
+    int* dst = p.out_table + static_cast<size_t>(y0) * p.max_pages;
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-        const int y = y0 + k, n = taken(k);
-        int* dst = p.out_table + static_cast<size_t>(y) * p.max_pages;
-        if (VEC && col(3) < n) {
+    for (int k = 0; k < ROWS; ++k, dst += p.max_pages) {
+        const int n = s_take[k];
+        if (VEC && col(U - 1) < n) {
             *reinterpret_cast<int4*>(dst + col(0)) = make_int4(e[k][0], e[k][1 % U], e[k][2 % U], e[k][3 % U]);
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (col(u) < n) dst[col(u)] = e[k][u];
         }
-    }
-    if (blockIdx.x == 0 && tid < ROWS && y0 + tid < p.rows_out) {
-        const int y = y0 + tid, len = s_new[tid];
-        p.out_lens[y] = len < 0 ? -1 : len;
-        p.copy_src[y] = -1;
-        p.copy_dst[y] = -1;
-        p.ws.rows[y] = s_elder[tid] && has_partial(len, p.shift, p.max_pages);
-        if (y == 0) p.ws.head->status = 0;
     }
 }
 
@@ -745,10 +750,22 @@ __global__ void __launch_bounds__(pg::THREADS) compact_apply_kernel(const Compac
     if (counts) {
         pdl_wait_primary();
         const int moves = p.ws.head->moves;
-        for (long long k = j00; k < moves; k += stride) {
-            const int s = p.copy_src[k], d = p.copy_dst[k];
-            p.pool.refs[d] = p.pool.refs[s];
-            p.pool.refs[s] = 0;
+        for (long long k0 = j00; k0 < moves; k0 += 8 * stride) {   // eight at a time
+            int from[8], to[8], n[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const long long k = k0 + u * stride;
+                from[u] = k < moves ? p.copy_src[k] : -1;
+                to[u] = k < moves ? p.copy_dst[k] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) n[u] = from[u] >= 0 ? p.pool.refs[from[u]] : 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (from[u] >= 0) {
+                    p.pool.refs[to[u]] = n[u];
+                    p.pool.refs[from[u]] = 0;
+                }
         }
         return;
     }

@@ -467,8 +467,8 @@ int gad_linear_status(int* status, void* stream);
  *
  *   logits      [G W, V] of `dtype` (GAD_DTYPE_BF16, _F16 or _F32), rows
  *               row_stride >= V values apart, aligned to the element size
- *   scores      float32 [G W]; -infinity: a beam without candidates (at the
- *               first step, all beams but one)
+ *   scores      float32 [G W]; -infinity (or another value that is not finite):
+ *               a beam without candidates (at the first step, all beams but one)
  *   finished    uint8 [G W], nonzero for finished beams, or NULL
  *   pad_token   the token of a finished beam's candidate, 0 <= pad_token < V
  *   out_scores  float32 [G, K]: scores, best first
@@ -481,9 +481,11 @@ int gad_linear_status(int* status, void* stream);
  *               calls that overlap on the GPU need different ones
  *
  * Scores are compared in 64 bits and rounded to float32 on output; equal
- * scores go to the lower w * V + v.  A logit of -infinity or NaN is never
- * chosen; a beam whose logits hold a NaN or +infinity has no log-sum and thus
- * no candidates.  Places that no candidate fills get score -infinity and
+ * scores go to the lower w * V + v.  (A beam offers its K largest logits, ties to
+ * the lower token: beside a score above about 1e9 in magnitude, where 64 bits
+ * no longer tell its logits apart, that is the order that counts.)  A logit of
+ * -infinity or NaN is never chosen; a beam whose logits hold a NaN or +infinity
+ * has no log-sum and thus no candidates.  Places that no candidate fills get score -infinity and
  * parent and token -1.  Outputs may not overlap scores (GAD_ERR_UNSUPPORTED).
  * Asynchronous on `stream`, allocates nothing, graph-capturable.
  */

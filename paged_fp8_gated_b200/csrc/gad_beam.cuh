@@ -4,8 +4,8 @@
 //   score(w, v) = s_w + (x_wv - lse_w),   lse_w = log sum_v exp(x_wv)
 //
 // for the logits x of beam w and its score s_w so far; a finished beam has the
-// one candidate (pad token, s_w).  The K highest scores are wanted in order,
-// ties by the lower w V + v.
+// one candidate (pad token, s_w), a beam whose score is not finite none.  The K
+// highest scores are wanted in order, ties by the lower w V + v.
 //
 // The order within a beam is that of its logits, so one pass over the logits
 // suffices: each block takes a segment of a row and leaves its K best logits,
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamPa
     pdl_launch_dependents();
     {   // a finished beam's logits and those of a dead one are not needed
         const float s = p.scores[row];
-        if ((p.finished != nullptr && p.finished[row] != 0) || !(s > NEG_INF)) return;
+        if ((p.finished != nullptr && p.finished[row] != 0) || !isfinite(s)) return;
     }
     if (tid == 0) s_n = 0;
     const T* x = static_cast<const T*>(p.logits) + row * p.ld;
@@ -388,8 +388,8 @@ __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamPa
 // One block per request.
 __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParams p) {
     using namespace bm;
-    __shared__ double s_lse[MAX_K], s_cum[MAX_K];   // per beam; a beam without candidates has lse NaN
-    __shared__ uint8_t s_done[MAX_K];
+    __shared__ double s_lse[MAX_K], s_cum[MAX_K];   // per beam
+    __shared__ uint8_t s_done[MAX_K];               // 0: a beam that goes on, 1: without candidates, 2: finished
     __shared__ double s_score[MERGE_BUF];
     __shared__ int s_flat[MERGE_BUF], s_n;
     const int tid = threadIdx.x, lane = tid & 31, g = blockIdx.x;
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
         const float cum = p.scores[row];
         const bool done = p.finished != nullptr && p.finished[row] != 0;
         double lse = 0;
-        if (!done && cum > NEG_INF) {
+        if (!done && isfinite(cum)) {
             float m = fmaxf(mine.x, NEG_INF);
             for (int s = lane + 32; s < p.S; s += 32) m = fmaxf(m, ms[s].x);
 #pragma unroll
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
         if (lane == 0) {
             s_lse[w] = lse;
             s_cum[w] = cum;
-            s_done[w] = done ? 2 : (cum > NEG_INF ? 0 : 1);
+            s_done[w] = !isfinite(cum) ? 1 : done ? 2 : 0;
         }
     }
     __syncthreads();

@@ -231,6 +231,7 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
             const int own = (nk + (1 << k) - 1) >> k;
             const bool promote = f32 && own > kLongChain;
             if (promote && bn != 128) continue;
+            if (k > 0 && tiles > cap.wide[k]) continue;   // a second wave of clusters costs more than it saves
             Plan q;
             q.kind = Plan::WIDE;
             q.bn = bn;

@@ -135,6 +135,41 @@ def test_beam_extreme_scores(cuda_dev):
     assert (np.abs(s.cpu().numpy() - rs) <= 2.0 ** -23 * np.abs(rs) + 1e-2).all()
 
 
+def test_beam_scores_that_are_not_finite(cuda_dev):
+    """Beams whose score is infinite or NaN have no candidates, finished or not."""
+    from paged_fp8_gated_b200 import binding
+    logits, scores, _ = _inputs(3, 4, 3000, "bf16", 60)
+    finished = torch.zeros(3, 4, dtype=torch.bool, device="cuda")
+    scores[0, 1], scores[1, 0], scores[1, 3], scores[2, :] = INF, float("nan"), -INF, INF
+    finished[1, 3] = finished[2, 0] = finished[0, 2] = True
+    s, p, t = binding.beam_select(logits, scores, 5, finished=finished, pad_token=7)
+    live = torch.where(scores.isfinite(), scores, -INF)
+    rs, rp, rt = P.beam(logits, live, 5, finished, 7)
+    assert np.array_equal(p.cpu().numpy(), rp) and np.array_equal(t.cpu().numpy(), rt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_beam_offsets_past_32_bits(dtype, cuda_dev):
+    """Rows 2^30 values apart, and the largest vocabulary."""
+    from paged_fp8_gated_b200 import binding
+    G, V, stride = (5, 3001, 1 << 30) if dtype == "bf16" else (3, 3001, 1 << 30)
+    logits, scores, g = _inputs(G, 1, V, dtype, 70)
+    big = torch.empty((G - 1) * stride + V, dtype=DT[dtype], device="cuda")
+    view = big.as_strided((G, 1, V), (stride, stride, 1))
+    view.copy_(logits)
+    a = binding.beam_select(view, scores, 4)
+    b = binding.beam_select(logits, scores, 4)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    del big, view
+    V = 1 << 24
+    x = torch.randn(1, 1, V, generator=g, device="cuda").to(DT[dtype])
+    x[0, 0, [V - 1, 5, V // 2]] = torch.tensor([30.0, 31.0, 29.0], device="cuda", dtype=DT[dtype])
+    s, p, t = binding.beam_select(x, torch.zeros(1, 1, device="cuda"), 3)
+    assert t.tolist() == [[5, V - 1, V // 2]] and p.tolist() == [[0, 0, 0]]
+    ref = torch.log_softmax(x.double().reshape(-1), 0)[[5, V - 1, V // 2]]
+    assert bool(((s.double() - ref).abs() <= 2.0 ** -24 * ref.abs() + 7e-6).all())
+
+
 def test_beam_workspace_poison_streams_and_graph(cuda_dev):
     from paged_fp8_gated_b200 import binding
     G, W, V, K = 4, 3, 12000, 5

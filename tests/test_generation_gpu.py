@@ -102,3 +102,32 @@ def test_beam_search_over_the_paged_cache(page_size, window, cuda_dev):
     B.pages_free(table, lens, refs, page_size)
     assert int(refs.abs().sum()) == 0 and lens.tolist() == [-1] * (G * K)
     assert B.linear_status() == 0
+
+
+@pytest.mark.parametrize("page_size", [1, 64])
+def test_step_with_empty_rows(page_size, cuda_dev):
+    """Rows without a request in the batch: the step writes no cache row for them, and the
+    other rows' outputs are those of a batch without them."""
+    from paged_fp8_gated_b200 import binding as B
+    from tests import helpers as H
+    R, num_pages, max_pages = 5, 600 if page_size == 1 else 12, 120 if page_size == 1 else 3
+    g = torch.Generator(device="cuda").manual_seed(9)
+    scale = torch.ones(1, device="cuda")
+    live = [1, 3, 4]
+    outs = {}
+    for rows in (list(range(R)), live):
+        kc, vc = (torch.zeros(num_pages, page_size, 2, 64, dtype=torch.uint8, device="cuda") for _ in range(2))
+        refs = torch.zeros(num_pages, dtype=torch.int32, device="cuda")
+        table = torch.full((len(rows), max_pages), -1, dtype=torch.int32, device="cuda")
+        lens = torch.tensor([0 if r in live else -1 for r in rows], dtype=torch.int32, device="cuda")
+        g.manual_seed(9)
+        for step, L in enumerate((8, 8, 1, 5, 1)):
+            qkv = torch.randn(R, L, W.QKV_COLS, generator=g, device="cuda").bfloat16()[rows].reshape(-1, W.QKV_COLS)
+            pos, loc = B.pages_extend(table, lens, refs, page_size, L)
+            out = B.attn_decode(qkv, pos, None, table, loc, kc, vc, scale, scale, page_size, 0, True, L=L)
+            outs.setdefault(step, []).append(out[[rows.index(r) for r in live]].float())
+        assert int((refs != 0).sum()) == sum(-(-23 // page_size) for _ in live)
+        written = kc.reshape(num_pages, -1).ne(0).any(1) | vc.reshape(num_pages, -1).ne(0).any(1)
+        assert bool((written == (refs != 0)).all())
+    for a, b in outs.values():
+        assert bool(((a - b).abs() <= H.ATOL + H.RTOL * b.abs()).all())

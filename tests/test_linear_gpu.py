@@ -149,3 +149,97 @@ def test_linear_refusals(cuda_dev):
         kw = dict(dict(x=x, w=w, bias=b, residual=r), **over)
         with pytest.raises(err or binding.GadError):
             binding.linear(kw.pop("x"), kw.pop("w"), **kw)
+
+
+# every form of the two kernels (a block or a cluster over K, pairs of 256 and 128
+# columns, pairs that share a tile), for 16-bit results and for fp32 ones, which are
+# promoted where the chains are long
+FORMS = [(520, 72, 8200), (520, 2056, 4099), (1, 72, 65), (130, 2056, 8200), (1, 2056, 8200), (70, 2056, 8200),
+         (1, 520, 65), (130, 8200, 2050), (1, 4104, 4099), (70, 4104, 2050), (1, 2056, 65), (1, 8200, 65),
+         (300, 72, 2050), (300, 1000, 2050), (70, 72, 65), (100, 2056, 2050), (70, 200, 65), (70, 4104, 65),
+         (1030, 520, 2050), (1030, 4104, 1001), (2100, 8200, 130)]
+
+
+@pytest.mark.parametrize("shape", FORMS, ids=str)
+def test_linear_forms(shape, cuda_dev):
+    from paged_fp8_gated_b200 import binding
+    x, w, b, r = _inputs(*shape, "fp16", "fp16", True, True, 11 + sum(shape))
+    _check(binding.linear(x, w, bias=b, residual=r, activation="silu"), x, w, b, r, "silu")
+    y = binding.linear(x, w, bias=b, residual=r.float(), activation="silu", out_dtype=torch.float32)
+    _check(y, x, w, b, r.float(), "silu")
+    assert binding.linear_status() == 0
+
+
+@pytest.mark.parametrize("shape", FORMS, ids=str)
+def test_linear_fp32_sums_do_not_lose_with_k(shape, cuda_dev):
+    """A fp32 result's error does not grow with K: no chain is longer than 768 products
+    (48 steps of 16, each cut off by at most 2^-23 of the magnitudes summed so far, and 8
+    more for the sums inside a step), and the chains are added up rounding to nearest."""
+    from paged_fp8_gated_b200 import binding
+    x, w, _, _ = _inputs(*shape, "bf16", "fp32", False, False, 12 + sum(shape))
+    y = binding.linear(x, w, out_dtype=torch.float32).double()
+    mag = x.double().abs() @ w.double().abs().T
+    bound = (56 * 2.0 ** -23 + (shape[1] / 512 + 8) * 2.0 ** -24) * mag
+    assert bool(((y - x.double() @ w.double().T).abs() <= bound).all())
+
+
+def test_linear_captured_behind_a_join(cuda_dev):
+    """Captured behind work of two joined streams, which it must wait for."""
+    from paged_fp8_gated_b200 import binding
+    x, w, _, _ = _inputs(64, 2048, 2304, "bf16", "bf16", False, False, 31)
+    want = binding.linear(x, w)
+    xs, ws, y = torch.zeros_like(x), torch.zeros_like(w), torch.empty_like(want)
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            ws.copy_(w)
+        xs.copy_(x)
+        torch.cuda.current_stream().wait_stream(side)
+        binding.linear(xs, ws, out=y)
+    for _ in range(3):
+        xs.zero_()
+        ws.zero_()
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+def test_linear_chain_of_dependent_calls(cuda_dev):
+    """Each call reads what the one before wrote, the weights too: back to back they give
+    what they give one at a time."""
+    from paged_fp8_gated_b200 import binding
+    x, w, _, _ = _inputs(64, 64, 64, "bf16", "bf16", False, False, 41)
+
+    def chain(wait):
+        a, b, every = x, w, []
+        for _ in range(8):
+            a = binding.linear(a, b)
+            if wait:
+                torch.cuda.synchronize()
+            b = binding.linear(b, a)
+            if wait:
+                torch.cuda.synchronize()
+            every += [a, b]
+        return every
+    want = chain(True)
+    for _ in range(5):
+        got = chain(False)
+        torch.cuda.synchronize()
+        # the same bits (towards the end the values outgrow the type: NaN compares too)
+        assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("T,N", [(9, 70), (24_000, 264)])
+def test_linear_offsets_past_32_bits(T, N, cuda_dev):
+    """Rows of y and residual so far apart that their offsets pass 2^32 values."""
+    from paged_fp8_gated_b200 import binding
+    K, ld = 64, -(-(1 << 32) // (T - 1)) // 8 * 8 + 8
+    x, w, b, r = _inputs(T, K, N, "bf16", "bf16", True, True, 51)
+    big = torch.empty((T - 1) * ld + N, dtype=torch.bfloat16, device="cuda")
+    y = big.as_strided((T, N), (ld, 1))
+    y.copy_(r)
+    binding.linear(x, w, bias=b, residual=y, out=y)
+    assert torch.equal(y, binding.linear(x, w, bias=b, residual=r))

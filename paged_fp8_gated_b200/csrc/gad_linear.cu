@@ -40,18 +40,23 @@ int linear_status_word(int** out) {
 }
 
 // [rows, K] 16-bit matrix, rows ld apart, in boxes of 64 x box_rows.
-int encode_rows(CUtensorMap* map, const void* base, bool fp16, int K, int rows, long long ld, int box_rows) {
+// Tiles of box_cols x box_rows of a matrix of 16-bit values, box_cols of them the
+// swizzle's width.
+int encode_tiles(CUtensorMap* map, const void* base, bool fp16, int cols, int rows, long long ld, int box_cols,
+                 int box_rows) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     const int st = tensor_map_encoder(&fn);
     if (st != GAD_OK) return st;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-    const cuuint32_t box[2] = {gad::lin::BK, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                     const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    box_cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                    : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : CU_TENSOR_MAP_SWIZZLE_32B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(GAD_ERR_CUDA, "cuTensorMapEncodeTiled (linear) failed (%d)", static_cast<int>(r));
     return GAD_OK;
 }
@@ -126,7 +131,7 @@ int capacity_of(OncePerContext& once, int smem, int cluster, int* out) {
     return GAD_OK;
 }
 
-OncePerContext g_narrow_smem[4], g_wide_smem[8];
+OncePerContext g_narrow_smem[4];
 
 // Asked once per (device, context); two threads that ask at the same time store
 // the same answers.
@@ -264,8 +269,8 @@ int launch_narrow(gad::lin::Params p, const void* x, long long ldx, const void* 
     int st = raise_smem(reinterpret_cast<const void*>(kern), g_narrow_smem[ACC / 32 > 2 ? 3 : ACC / 32], kSmemMax);
     if (st != GAD_OK) return st;
     CUtensorMap wmap, xmap;
-    st = encode_rows(&wmap, w, p.fp16 != 0, p.K, p.N, ldw, ROWS);
-    if (st == GAD_OK) st = encode_rows(&xmap, x, p.fp16 != 0, p.K, p.T, ldx, p.tt);
+    st = encode_tiles(&wmap, w, p.fp16 != 0, p.K, p.N, ldw, BK, ROWS);
+    if (st == GAD_OK) st = encode_tiles(&xmap, x, p.fp16 != 0, p.K, p.T, ldx, BK, p.tt);
     if (st != GAD_OK) return st;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
@@ -278,44 +283,42 @@ int launch_narrow(gad::lin::Params p, const void* x, long long ldx, const void* 
     return GAD_OK;
 }
 
-template <int BN, bool SPLIT, bool PROMOTE>
-int launch_wide(gad::lin::Params p, const void* x, long long ldx, const void* w, long long ldw, const Plan& plan, int sms,
-                cudaStream_t s) {
+template <int BN, int S, bool PROMOTE>
+int launch_wide(gad::lin::Params p, const void* x, long long ldx, const void* w, long long ldw, int sms, cudaStream_t s) {
     using namespace gad::lin;
-    auto kern = gad::linear_wide_kernel<BN, SPLIT, PROMOTE>;
-    static_assert(Wide<BN, SPLIT, PROMOTE>::SMEM <= kSmemMax, "ring and staging fit");
-    int st = raise_smem(reinterpret_cast<const void*>(kern), g_wide_smem[(BN == 256) + 2 * SPLIT + 4 * PROMOTE], kSmemMax);
+    using C = Wide<BN, S, PROMOTE>;
+    auto kern = gad::linear_wide_kernel<BN, S, PROMOTE>;
+    static_assert(C::SMEM <= kSmemMax, "ring and staging fit");
+    static OncePerContext raised;
+    int st = raise_smem(reinterpret_cast<const void*>(kern), raised, kSmemMax);
     if (st != GAD_OK) return st;
     p.mt = (p.T + 255) / 256;
     p.nt = (p.N + BN - 1) / BN;
-    p.split = plan.split;
     const long long tiles = static_cast<long long>(p.mt) * p.nt;
-    CUtensorMap wmap, xmap;
-    st = encode_rows(&wmap, w, p.fp16 != 0, p.K, p.N, ldw, BN / 2);
-    if (st == GAD_OK) st = encode_rows(&xmap, x, p.fp16 != 0, p.K, p.T, ldx, ROWS);
+    CUtensorMap wmap, xmap, ymap;
+    st = encode_tiles(&wmap, w, p.fp16 != 0, p.K, p.N, ldw, BK, BN / 2);
+    if (st == GAD_OK) st = encode_tiles(&xmap, x, p.fp16 != 0, p.K, p.T, ldx, BK, ROWS);
+    if (st == GAD_OK && p.by_tma) st = encode_tiles(&ymap, p.y, p.fp16 != 0, p.N, p.T, p.ldy, C::BOX, 32);
+    else std::memset(&ymap, 0, sizeof(ymap));
     if (st != GAD_OK) return st;
-    const long long pairs = SPLIT ? tiles * plan.split : tiles < sms / 2 ? tiles : sms / 2;
+    const long long pairs = S > 1 ? tiles * S : tiles < sms / 2 ? tiles : sms / 2;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     // all of an SM's shared memory: alone there, so its tensor memory is free
-    cluster_config(&cfg, attr, static_cast<unsigned>(2 * pairs), 1, WIDE_THREADS, smem_share(512), 2 * plan.split, s);
+    cluster_config(&cfg, attr, static_cast<unsigned>(2 * pairs), 1, WIDE_THREADS, smem_share(512), 2 * S, s);
     attr[1] = pdl_attr();
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, wmap, xmap, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, wmap, xmap, ymap, p);
     if (e != cudaSuccess) return fail(GAD_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));
     return GAD_OK;
 }
 
-template <bool PROMOTE>
-int launch_wide(const gad::lin::Params& p, const void* x, long long ldx, const void* w, long long ldw, const Plan& plan,
-                int sms, cudaStream_t s) {
-    if constexpr (!PROMOTE) {
-        if (plan.bn == 256)
-            return plan.split > 1 ? launch_wide<256, true, false>(p, x, ldx, w, ldw, plan, sms, s)
-                                  : launch_wide<256, false, false>(p, x, ldx, w, ldw, plan, sms, s);
-    }
-    return plan.split > 1 ? launch_wide<128, true, PROMOTE>(p, x, ldx, w, ldw, plan, sms, s)
-                          : launch_wide<128, false, PROMOTE>(p, x, ldx, w, ldw, plan, sms, s);
+template <int BN, bool PROMOTE>
+int launch_wide(const gad::lin::Params& p, const void* x, long long ldx, const void* w, long long ldw, int split, int sms,
+                cudaStream_t s) {
+    return split == 1   ? launch_wide<BN, 1, PROMOTE>(p, x, ldx, w, ldw, sms, s)
+           : split == 2 ? launch_wide<BN, 2, PROMOTE>(p, x, ldx, w, ldw, sms, s)
+                        : launch_wide<BN, 4, PROMOTE>(p, x, ldx, w, ldw, sms, s);
 }
 
 }  // namespace
@@ -371,6 +374,7 @@ int gad_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const voi
     p.vec = ldy % 4 == 0 && aligned(y, 4 * oe) && (!residual || (ldr % 4 == 0 && aligned(residual, 4 * oe)));
     const int chunk = 16 / oe;
     p.vec16 = ldy % chunk == 0 && aligned(y, 16) && (!residual || (ldr % chunk == 0 && aligned(residual, 16)));
+    p.by_tma = oe == 2 && p.vec16 && !residual;
     st = linear_status_word(&p.err);
     if (st != GAD_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -379,8 +383,9 @@ int gad_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const voi
     if (st != GAD_OK) return st;
     const Plan plan = choose(T, K, N, out_dtype == GAD_DTYPE_F32, cap, sms);
     if (plan.kind == Plan::WIDE)
-        return plan.promote ? launch_wide<true>(p, x, ldx, w, ldw, plan, sms, s)
-                            : launch_wide<false>(p, x, ldx, w, ldw, plan, sms, s);
+        return plan.promote     ? launch_wide<128, true>(p, x, ldx, w, ldw, plan.split, sms, s)
+               : plan.bn == 128 ? launch_wide<128, false>(p, x, ldx, w, ldw, plan.split, sms, s)
+                                : launch_wide<256, false>(p, x, ldx, w, ldw, plan.split, sms, s);
     if (!plan.promote) return launch_narrow<0>(p, x, ldx, w, ldw, plan, s);
     switch (gad::lin::narrow_acc(narrow_tokens(T))) {
         case 32: return launch_narrow<32>(p, x, ldx, w, ldw, plan, s);

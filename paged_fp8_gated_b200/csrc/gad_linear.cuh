@@ -218,15 +218,27 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 // (the aligned forms need the warp converged, which code with divergent loops
 // before them does not promise by itself)
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
 }
-// The same without the release: nothing that the thread wrote is read behind it.
-// (A release waits for the thread's stores to y: a thousand cycles and more.)
-__device__ __forceinline__ void cluster_sync_relaxed() {
+__device__ __forceinline__ void cluster_arrive_relaxed() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
+}
+// Without the release: nothing that the thread wrote is read behind it.  (A
+// release waits for the thread's stores to y: a thousand cycles and more.)
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    cluster_arrive_relaxed();
+    cluster_wait();
 }
 // The address of `addr` (this block's shared memory) in block `rank` of the cluster.
 __device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
@@ -471,7 +483,6 @@ __device__ __forceinline__ void write_edge(const Params& p, const uint8_t* tile,
 }
 template <int OUT, int CW>
 __device__ __forceinline__ void write_piece(const Params& p, const uint8_t* tile, long long t0, int n0, int lane) {
-    if (t0 >= p.T) return;
     if (p.vec16 && n0 + CW <= p.N) write_tile<OUT, CW>(p, tile, t0, n0, lane);
     else write_edge<OUT, CW>(p, tile, t0, n0, lane);
 }
@@ -520,6 +531,10 @@ template <int BN, int S, bool PROMOTE, class Get, class Last>
 __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* y_map, uint8_t* stage, uint16_t* strip,
                                             long long row0, int col0, int lane, Get get, Last last) {
     using C = Wide<BN, S, PROMOTE>;
+    if (row0 >= p.T) {
+        last();
+        return;
+    }
     if (!PROMOTE && p.by_tma) {
         if (lane == 0) tma_store_wait_read();   // the tile before has left its boxes
 #pragma unroll 1
@@ -539,7 +554,7 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
         last();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && row0 < p.T) {
+        if (lane == 0) {
 #pragma unroll
             for (int blk = 0; blk < C::OWN / C::BOX; ++blk)
                 if (col0 + blk * C::BOX < p.N)
@@ -832,6 +847,21 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
     const int k_first = static_cast<int>(static_cast<long long>(nk_all) * part / S);
     const int nk = static_cast<int>(static_cast<long long>(nk_all) * (part + 1) / S) - k_first;
 
+    // tile -> (token tile, weight tile): WIDE_GROUP token tiles sweep N together,
+    // so the pairs at work at one time share rows of x and of w in L2
+    auto place = [&](int tile, int* m, int* n) {
+        const int per = WIDE_GROUP * p.nt, g = tile / per, in = tile - g * per;
+        const int gm = p.mt - g * WIDE_GROUP < WIDE_GROUP ? p.mt - g * WIDE_GROUP : WIDE_GROUP;
+        *m = g * WIDE_GROUP + in % gm;
+        *n = in / gm;
+    };
+    // S > 1: the only tile, its first token in this block, and how many of the four
+    // epilogue quads have tokens (only those exchange sums)
+    int m_only = 0, n_only = 0;
+    if (S > 1) place(pair, &m_only, &n_only);
+    const long long t_only = static_cast<long long>(m_only) * 256 + rank * ROWS;
+    const int quads = t_only >= p.T ? 0 : p.T - t_only >= ROWS ? 4 : static_cast<int>(p.T - t_only + 31) / 32;
+
     if (tid == 0) {
         tma_prefetch_map(&w_map);
         tma_prefetch_map(&x_map);
@@ -847,7 +877,7 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
         mbar_init(RECEIVED, 1);
         *abort_flag = 0;
         mbar_fence_init();
-        if (S > 1) mbar_arrive_expect_tx(RECEIVED, C::RECV);
+        if (S > 1) mbar_arrive_expect_tx(RECEIVED, C::RECV / 4 * static_cast<uint32_t>(quads));
     }
     if (warp == 2) {
         tc2_alloc(smem_addr(tmem_slot), COLS);
@@ -861,15 +891,6 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
     pdl_launch_dependents();
     pdl_wait_primary();
 
-    // tile -> (token tile, weight tile): WIDE_GROUP token tiles sweep N together,
-    // so the pairs at work at one time share rows of x and of w in L2
-    auto place = [&](int tile, int* m, int* n) {
-        const int per = WIDE_GROUP * p.nt, g = tile / per, in = tile - g * per;
-        const int gm = p.mt - g * WIDE_GROUP < WIDE_GROUP ? p.mt - g * WIDE_GROUP : WIDE_GROUP;
-        *m = g * WIDE_GROUP + in % gm;
-        *n = in / gm;
-    };
-
     // Epilogue warps: 32 tokens, and half of the columns that the pair finishes.
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
@@ -877,6 +898,10 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
     uint16_t* strip = reinterpret_cast<uint16_t*>(smem + C::STRIPS + (warp - 4) * 128);
     // its pieces in slot `slot` of the sent or received ones
     auto piece = [&](uint8_t* from, int slot) { return from + slot * C::SLOT + (warp - 4) * C::PIECES * C::PIECE; };
+
+    float acc[PROMOTE ? BN / 2 : 1];   // PROMOTE: the sums
+    uint32_t src = 0;                  // the warp's first column of the first pair's share
+    bool summed = true;                // they are there
 
     if (warp == 0) {
         if (lane == 0) {
@@ -935,15 +960,12 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
         }
     } else if (warp >= 4) {
         int local = 0;
-        bool ok = true;
-        for (int tile = pair; tile < tiles && ok; tile += pairs) {
-            float acc[PROMOTE ? BN / 2 : 1];
+        for (int tile = pair; tile < tiles && summed; tile += pairs) {
             const int chains = PROMOTE ? (nk + SEG - 1) / SEG : 1;
             if (PROMOTE) {
 #pragma unroll
                 for (int j = 0; j < BN / 2; ++j) acc[j] = 0.f;
             }
-            uint32_t src = 0;   // the warp's first column of the first pair's share
             auto release = [&] {   // the accumulator has been read
                 tc_fence_before();
                 __syncwarp();
@@ -952,8 +974,8 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
             for (int c = 0; c < chains; ++c) {
                 const int b = local & 1;
                 const bool got = wait_bounded(TFULL(b), (local / 2) & 1, abort_flag);
-                ok = __all_sync(0xffffffffu, got);
-                if (!ok) break;
+                summed = __all_sync(0xffffffffu, got);
+                if (!summed) break;
                 ++local;
                 tc_fence_after();
                 src = lanes + static_cast<uint32_t>(BN * b + C::OWN * half);
@@ -969,36 +991,7 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
                     release();
                 }
             }
-            if (!ok) break;
-            if (S > 1) {
-                // the other pairs' columns of its sums, for them to fetch; its MMAs
-                // are done, so the ring is free
-#pragma unroll(PROMOTE ? S : 1)
-                for (int d = 0; d < S; ++d) {
-                    if (!PROMOTE && d == part) continue;
-                    uint8_t* to = piece(smem, PROMOTE ? d : d - (d > part));
-#pragma unroll(PROMOTE ? C::OWN / 16 : 1)
-                    for (int j = 0; j < C::OWN; j += 16) {
-                        float v[16];
-                        if (PROMOTE) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = acc[PROMOTE ? d * C::OWN + j + e : 0];
-                        } else {
-                            uint32_t raw[16];
-                            tc_ld16(src + static_cast<uint32_t>(d * (BN / S) + j), raw);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(raw[e]);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<float4*>(to + j / C::CW * C::PIECE + swizzled<C::CW * 4>(lane, j % C::CW / 4 + k)) =
-                                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                    }
-                }
-                fence_proxy_async_smem();
-                break;   // its only tile
-            }
+            if (!summed || S > 1) break;   // (S > 1: its only tile)
             int m, n;
             place(tile, &m, &n);
             wide_finish<BN, S, PROMOTE>(
@@ -1031,8 +1024,37 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
         for (uint32_t b = 0; b < 2 * S; ++b)
             if (b != crank) st_cluster_u32(in_block(smem_addr(ends + crank), b), ends[crank]);
     }
-    if (warp == 0) cluster_sync();
-    else cluster_sync_relaxed();
+    if (warp == 0) cluster_arrive();
+    else cluster_arrive_relaxed();
+    if (S > 1 && warp >= 4 && summed && quad < quads) {
+        // the other pairs' columns of this one's sums, for them to have; its MMAs are
+        // done, so its ring is free
+#pragma unroll(PROMOTE ? S : 1)
+        for (int d = 0; d < S; ++d) {
+            if (!PROMOTE && d == part) continue;
+            uint8_t* to = piece(smem, PROMOTE ? d : d - (d > part));
+#pragma unroll(PROMOTE ? C::OWN / 16 : 1)
+            for (int j = 0; j < C::OWN; j += 16) {
+                float v[16];
+                if (PROMOTE) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = acc[PROMOTE ? d * C::OWN + j + e : 0];
+                } else {
+                    uint32_t raw[16];
+                    tc_ld16(src + static_cast<uint32_t>(d * (BN / S) + j), raw);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(raw[e]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    *reinterpret_cast<float4*>(to + j / C::CW * C::PIECE + swizzled<C::CW * 4>(lane, j % C::CW / 4 + k)) =
+                        make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+        }
+        fence_proxy_async_smem();
+    }
+    cluster_wait();
     // All loads were used, so have landed, unless a block gave up.  Then each pair's
     // first block waits for the ones in flight, on its barriers: for a stage that
     // only one block has asked for, it makes up what the barrier still expects.
@@ -1056,7 +1078,7 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
     if (S > 1) {
         // every block's ring is idle: the pieces go to the pairs that finish them (of
         // a pair that gave up too, whatever they are: none waits for what never comes)
-        if (warp >= 4) {
+        if (warp >= 4 && quad < quads) {
             uint8_t* received = smem + C::SENT;
             if (lane == 0) {
 #pragma unroll 1
@@ -1070,12 +1092,9 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
             const bool got = wait_bounded(RECEIVED, 0, abort_flag, false, LAST_LIMIT_NS);
             tc_fence_after();
             if (__all_sync(0xffffffffu, got && !gave_up)) {
-                int m, n;
-                place(pair, &m, &n);
                 const int first = part * (BN / S);
                 wide_finish<BN, S, PROMOTE>(
-                    p, &y_map, stage, strip, static_cast<long long>(m) * 256 + rank * ROWS + quad * 32,
-                    n * BN + first + half * C::OWN, lane,
+                    p, &y_map, stage, strip, t_only + quad * 32, n_only * BN + first + half * C::OWN, lane,
                     [&](int at, float (&v)[16]) {   // its own sums, then the others' by rank
                         const int q = at / C::CW * C::PIECE, chunk = at % C::CW / 4;
                         if (PROMOTE) {

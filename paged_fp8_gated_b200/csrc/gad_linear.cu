@@ -177,19 +177,25 @@ int narrow_tokens(int T) {
 constexpr int kLongChain = 768 / gad::lin::BK;
 
 // The plan with the least time by this model of the kernels, in microseconds.
-// Its constants are fitted to both kernels at T = 1 .. 4,096 over nine (K, N)
-// from 256 x 32,000 to 8,192 x 32,001, cold weights:
-//   narrow: a stage takes a block 0.30 (an SM draws 54 GB/s of weights), or its
-//     bytes at an SM's 123 GB/s from L2, or all blocks' weights at 6.4 TB/s, or
-//     a load's latency (2.0) over the stages in flight; a block's fixed part is
-//     its cluster's start, its share of the epilogue and the exchange with the
-//     cluster.  Example: 32 x 8,192 x 2,304 (18 tiles) 42 / 23 / 14 / 12 in
-//     clusters of 1 / 2 / 4 / 8 blocks.
-//   wide: a stage of 256 x 256 takes a pair 0.33 (the tensor cores' time; 0.41
-//     when no other tile reads the same weights), one of 256 x 128 0.265 (an SM's
-//     share of L2 bandwidth).  Example: 768 x 8,192 x 2,304 44 on 27 of 74 pairs,
-//     29 with two pairs a tile; 1,024 x 8,192 x 2,304 (36 tiles, more than the 33
-//     clusters of four blocks that fit) 44 and 55.
+// Its constants are fitted to every plan at T = 1 .. 2,048 over ten (K, N) from
+// 256 x 32,000 to 8,192 x 32,000, weights from memory, launches one behind
+// another; the plan taken is there 0.7% slower than the fastest on average, 9% at
+// most:
+//   narrow: a stage takes a block 0.294 (an SM draws 56 GB/s of weights), or its
+//     bytes at an SM's 126 GB/s from L2, or all blocks' weights at 5.9 TB/s, or
+//     a load's latency (1.48) over the stages in flight; a block's fixed part is
+//     its cluster's start, its SM's share of the epilogue and the exchange with
+//     the cluster.  Blocks that leave room on their SM start while the launch
+//     before still runs.  Examples: 32 x 8,192 x 2,304 (18 tiles) 42 / 23 / 14 /
+//     12 in clusters of 1 / 2 / 4 / 8 blocks; 32 x 1,024 x 8,192 (64 tiles) 7.2
+//     in clusters of two blocks alone on their SMs, 8.3 of four, four to an SM.
+//   wide: a stage of 256 x 256 takes a pair 0.37 (the tensor cores' 0.33 in a
+//     long chain; 0.40 when no other tile reads the same weights), one of
+//     256 x 128 0.26 (an SM's share of L2 bandwidth).  Example: 768 x 8,192 x
+//     2,304 43 on 27 of 74 pairs, 27 with two pairs a tile; 1,024 x 8,192 x 2,304
+//     (36 tiles, more than the 33 clusters of four blocks that fit) 43 and 52.
+//   Promoted chains cost the one 17% and the other 10% (1,024 x 4,096 x 4,096 in
+//     fp32 41 and 43, 4,096 x 8,192 x 14,336 980 and 898).
 Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
     using namespace gad::lin;
     const int nk = (K + BK - 1) / BK;
@@ -197,6 +203,7 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
     auto take = [&](const Plan& q) {
         if (q.us < best.us) best = q;
     };
+    static constexpr double start[kClasses] = {1.88, 1.77, 1.61};
     const double dram = 2.0 * (static_cast<double>(T) * K + static_cast<double>(N) * K) / 6.4e6;
     {
         const int tt = narrow_tokens(T);
@@ -210,13 +217,13 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
                 if (promote && m > 1) continue;   // registers for two blocks
                 int stages = 1;
                 while (stages < own && stages < NARROW_MAX_STAGES && narrow_smem(tt, stages + 1) <= budget) ++stages;
-                const double fixed = 1.0 + 0.15 * c + tt * (0.012 + 0.016 / c + 0.004 * c);
                 auto wave = [&](double clusters) {
                     const double blocks = clusters * c, per_sm = std::fmax(1.0, std::ceil(blocks / sms));
-                    double ts = std::fmax(0.30, per_sm * narrow_stage(tt) / 123e3);
-                    ts = std::fmax(ts, blocks * TILE / 6.4e6);
-                    if (own > stages) ts = std::fmax(ts, 2.0 / stages);
-                    return own * ts + fixed;
+                    double ts = std::fmax(0.294, per_sm * narrow_stage(tt) / 126e3);
+                    ts = std::fmax(ts, blocks * TILE / 5.9e6);
+                    if (own > stages) ts = std::fmax(ts, 1.48 / stages);
+                    const double shared = m == 1 ? std::fmax(per_sm, 1.6) : per_sm;
+                    return own * ts + 1.07 + 0.073 * c + tt * (0.0064 + 0.0206 * shared / c + 0.0029 * c);
                 };
                 const long long fit = cap.narrow[m][k], full = tiles / fit, rest = tiles % fit;
                 Plan q;
@@ -224,18 +231,20 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
                 q.split = c;
                 q.cls = m;
                 q.promote = promote;
-                q.us = 2.4 + full * wave(static_cast<double>(fit)) + (rest ? wave(static_cast<double>(rest)) : 0.0);
+                q.us = start[m] + full * wave(static_cast<double>(fit)) + (rest ? wave(static_cast<double>(rest)) : 0.0);
+                if (promote) q.us *= 1.17;
                 take(q);
             }
         }
     }
-    const double stage256 = T <= 256 ? 0.41 : 0.33;
+    const double stage256 = T <= 256 ? 0.397 : 0.373;
     for (int bn = 256; bn >= 128; bn /= 2) {
         const double tiles = std::ceil(T / 256.0) * std::ceil(static_cast<double>(N) / bn);
         for (int k = 0; k < 3 && (1 << k) <= nk; ++k) {
             const int own = (nk + (1 << k) - 1) >> k;
             const bool promote = f32 && own > kLongChain;
             if (promote && bn != 128) continue;
+            if (bn == 256 && k == 2) continue;            // always behind 128 (512 x 8,192 x 1,024 19.3, 18.2)
             if (k > 0 && tiles > cap.wide[k]) continue;   // a second wave of clusters costs more than it saves
             Plan q;
             q.kind = Plan::WIDE;
@@ -244,10 +253,11 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
             q.promote = promote;
             const double waves = std::ceil(tiles / cap.wide[k]);
             if (k == 0)
-                q.us = bn == 256 ? 6.7 + waves * std::fmax(own * stage256, 3.0) : 5.0 + waves * std::fmax(own * 0.265, 1.9);
+                q.us = bn == 256 ? 4.4 + waves * std::fmax(own * stage256, 2.28) : 4.58 + waves * std::fmax(own * 0.2635, 1.4);
             else
-                q.us = 3.5 + waves * (bn == 256 ? own * stage256 + 5.3 : own * 0.22 + 2.5);
-            q.us = std::fmax(q.us, 3.5 + dram);
+                q.us = 3.7 + 0.6 * (k == 2) + (bn == 256 ? own * stage256 + 2.9 : own * 0.2166 + 1.5);
+            if (promote) q.us *= 1.1;
+            q.us = std::fmax(q.us, 1.9 + dram);
             take(q);
         }
     }
@@ -316,9 +326,11 @@ int launch_wide(gad::lin::Params p, const void* x, long long ldx, const void* w,
 template <int BN, bool PROMOTE>
 int launch_wide(const gad::lin::Params& p, const void* x, long long ldx, const void* w, long long ldw, int split, int sms,
                 cudaStream_t s) {
-    return split == 1   ? launch_wide<BN, 1, PROMOTE>(p, x, ldx, w, ldw, sms, s)
-           : split == 2 ? launch_wide<BN, 2, PROMOTE>(p, x, ldx, w, ldw, sms, s)
-                        : launch_wide<BN, 4, PROMOTE>(p, x, ldx, w, ldw, sms, s);
+    if (split == 1) return launch_wide<BN, 1, PROMOTE>(p, x, ldx, w, ldw, sms, s);
+    if constexpr (BN == 128) {
+        if (split == 4) return launch_wide<BN, 4, PROMOTE>(p, x, ldx, w, ldw, sms, s);
+    }
+    return launch_wide<BN, 2, PROMOTE>(p, x, ldx, w, ldw, sms, s);
 }
 
 }  // namespace
@@ -374,7 +386,8 @@ int gad_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const voi
     p.vec = ldy % 4 == 0 && aligned(y, 4 * oe) && (!residual || (ldr % 4 == 0 && aligned(residual, 4 * oe)));
     const int chunk = 16 / oe;
     p.vec16 = ldy % chunk == 0 && aligned(y, 16) && (!residual || (ldr % chunk == 0 && aligned(residual, 16)));
-    p.by_tma = oe == 2 && p.vec16 && !residual;
+    // (a TMA store writes a row to the end of its last 16 bytes)
+    p.by_tma = oe == 2 && p.vec16 && N % 8 == 0 && !residual;
     st = linear_status_word(&p.err);
     if (st != GAD_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

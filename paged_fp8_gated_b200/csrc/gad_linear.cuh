@@ -70,7 +70,7 @@ struct Params {
     int vec16;               // and of 16 bytes
     int tt, nstg;            // narrow: tokens per tile, ring stages
     int mt, nt;              // wide: tiles along the tokens and along N
-    int by_tma;              // wide: y leaves by TMA (16-bit values in 16-byte rows, no residual)
+    int by_tma;              // wide: y leaves by TMA (rows of whole 16 bytes of 16-bit values, no residual)
     int* err;                // status word: STATUS_LINEAR_WAIT when a bounded wait gave up
 };
 constexpr int STATUS_LINEAR_WAIT = 16;

@@ -16,11 +16,15 @@ pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BF16, F32 = 1, 6
 LINEAR = 16  # GAD_STATUS_LINEAR_WAIT
-# one block a tile; a cluster over K; promoted chains; pairs, with 256 and 128 columns;
-# pairs that share a tile; promoted pairs
+# one block a tile; a cluster over K; promoted chains, of 64, 128 and 256 tokens; pairs,
+# with 256 and 128 columns; two and four pairs that share a tile; promoted pairs, alone
+# and sharing
 CALLS = [("narrow", 8, 1024, 40000, BF16), ("cluster", 16, 8192, 1024, BF16), ("promote", 16, 8192, 8192, F32),
          ("wide", 2048, 1024, 4096, BF16), ("wide128", 256, 1024, 8192, BF16), ("split", 512, 8192, 1024, BF16),
-         ("wide_promote", 1024, 4096, 4096, F32)]
+         ("wide_promote", 1024, 4096, 4096, F32), ("promote128", 96, 8192, 4096, F32),
+         ("promote256", 160, 4096, 8192, F32), ("split256", 192, 2048, 8192, BF16), ("split4", 256, 8192, 1024, BF16),
+         ("promote_pairs", 96, 1024, 40000, F32), ("promote_split", 128, 4096, 4096, F32),
+         ("promote_split4", 128, 8192, 128, F32)]
 
 
 def test_linear_waits_give_up_and_report(cuda_dev):

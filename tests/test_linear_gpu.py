@@ -170,6 +170,34 @@ def test_linear_forms(shape, cuda_dev):
     assert binding.linear_status() == 0
 
 
+# pairs' tiles that end inside y's rows and columns: 256 and 128 columns, alone and two
+# or four pairs that share a tile
+EDGES = [(1300, 136, 2049), (300, 328, 9001), (193, 2056, 8203), (129, 1032, 8201), (450, 1032, 2001),
+         (250, 8200, 1003), (33, 520, 32001), (385, 72, 31), (1300, 136, 2056), (300, 328, 9008), (193, 2056, 8200),
+         (161, 2056, 8200), (129, 1032, 8200), (450, 1032, 2008), (250, 8200, 1000), (33, 520, 32008), (385, 72, 24)]
+
+
+@pytest.mark.parametrize("shape", EDGES, ids=str)
+@pytest.mark.parametrize("dtype,bias,act", [("bf16", False, "none"), ("fp16", True, "gelu")])
+def test_linear_rows_inside_wider_ones(shape, dtype, bias, act, cuda_dev):
+    """y's rows at 16-byte distances inside wider ones: nothing beside y is written, and
+    rows at odd distances get the same bits."""
+    from paged_fp8_gated_b200 import binding
+    T, K, N = shape
+    x, w, b, _ = _inputs(*shape, dtype, dtype, bias, False, 13 + sum(shape))
+    wide = torch.full((T + 2, (N + 7) // 8 * 8 + 16), 9.0, device="cuda", dtype=x.dtype)
+    y = wide[1:T + 1, 8:N + 8]
+    binding.linear(x, w, bias=b, activation=act, out=y)
+    _check(y.contiguous(), x, w, b, None, act)
+    assert bool((wide[0] == 9).all() and (wide[-1] == 9).all())
+    assert bool((wide[:, :8] == 9).all() and (wide[:, N + 8:] == 9).all())
+    odd = torch.full((T, N // 2 * 2 + 3), 9.0, device="cuda", dtype=x.dtype)
+    binding.linear(x, w, bias=b, activation=act, out=odd[:, 1:N + 1])
+    assert torch.equal(odd[:, 1:N + 1], y)
+    assert bool((odd[:, 0] == 9).all() and (odd[:, N + 1:] == 9).all())
+    assert binding.linear_status() == 0
+
+
 @pytest.mark.parametrize("shape", FORMS, ids=str)
 def test_linear_fp32_sums_do_not_lose_with_k(shape, cuda_dev):
     """A fp32 result's error does not grow with K: no chain is longer than 768 products

@@ -25,7 +25,13 @@
 //
 // Bound: one read of the logits; beside it one MUFU exponential per logit (16 a
 // cycle and SM: three quarters of the read's time for 16-bit logits) and about
-// four other instructions (maxima and sums in packed pairs).
+// four other instructions (maxima and sums in packed pairs).  Measured, both
+// kernels: 32 x 8 beams over 131,072 bf16 logits, K = 16, 21.5 us with the logits
+// in L2 and 27 from memory (a read at the copy rate 10.2, the exponentials 7.5,
+// about 8 the segment's end: threshold, second look, ranks, merge); 16 x 4 over
+// 32,001 fp32 10.6, 1 x 4 over 32,000 8.7, all latency.  Asking for lines ahead of
+// their load into L2 took 26 us from memory and 22.7 from L2, where a product has
+// just left them: not done.
 #pragma once
 
 #include <cstdint>

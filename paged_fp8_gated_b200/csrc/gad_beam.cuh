@@ -26,12 +26,12 @@
 // Bound: one read of the logits; beside it one MUFU exponential per logit (16 a
 // cycle and SM: three quarters of the read's time for 16-bit logits) and about
 // four other instructions (maxima and sums in packed pairs).  Measured, both
-// kernels: 32 x 8 beams over 131,072 bf16 logits, K = 16, 21.5 us with the logits
-// in L2 and 27 from memory (a read at the copy rate 10.2, the exponentials 7.5,
+// kernels: 32 x 8 beams over 131,072 bf16 logits, K = 16, 20.8 us with the logits
+// in L2 and 23 from memory (a read at the copy rate 10.2, the exponentials 7.5,
 // about 8 the segment's end: threshold, second look, ranks, merge); 16 x 4 over
-// 32,001 fp32 10.6, 1 x 4 over 32,000 8.7, all latency.  Asking for lines ahead of
-// their load into L2 took 26 us from memory and 22.7 from L2, where a product has
-// just left them: not done.
+// 32,001 fp32 10.3, 1 x 4 over 32,000 7.9, all latency.  Asking for lines ahead of
+// their load into L2 gained 1.3 us from memory and lost 1.2 from L2, where a product
+// has just left them: not done.
 #pragma once
 
 #include <cstdint>
@@ -147,22 +147,41 @@ __device__ __forceinline__ float value_of(uint64_t c) { return from_key(static_c
 __device__ __forceinline__ uint32_t index_of(uint64_t c) { return 0xffffffffu - static_cast<uint32_t>(c); }
 
 // A value that at least K of the threads' keys reach, and as far as their bits
-// tell them apart no more than K + K / 4 + 2: bisection over the key's bits, a
-// counting barrier a bit (about 12 of them, 200 cycles each; one warp alone
-// took 300 a bit, taking maxima out one by one 200 for each of the K).  All
-// threads call it; its first barrier also covers what they wrote before.
+// tell them apart no more than K + K / 4 + 2: bisection over the key's bits below
+// those that all finite keys share, a counting barrier a bit (about 5 of them, 200
+// cycles each; from the top bit on 12, one warp alone took 300 a bit, taking
+// maxima out one by one 200 for each of the K).  All threads call it, once; its
+// first barrier also covers what they wrote before.
 __device__ __forceinline__ uint32_t kth_key(uint32_t key, int K) {
-    uint32_t t = 0;
+    constexpr uint32_t NONE = 0x007fffffu;   // order_key(-inf)
+    __shared__ uint32_t s_lo[THREADS / 32], s_hi[THREADS / 32];
+    const bool some = key > NONE;
+    const uint32_t lo = __reduce_min_sync(0xffffffffu, some ? key : ~0u);
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, some ? key : 0u);
+    if ((threadIdx.x & 31) == 0) {
+        s_lo[threadIdx.x >> 5] = lo;
+        s_hi[threadIdx.x >> 5] = hi;
+    }
+    int c = __syncthreads_count(some);
+    if (c < K) return NONE;
+    uint32_t least = s_lo[0], most = s_hi[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w) {
+        least = min(least, s_lo[w]);
+        most = max(most, s_hi[w]);
+    }
+    int bit = 31 - __clz(static_cast<int>(least ^ most));   // -1: all the same
+    uint32_t t = bit < 0 ? most : most & ~((2u << bit) - 1);
 #pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
+    for (; bit >= 0 && c > K + K / 4 + 2; --bit) {
         const uint32_t up = t | 1u << bit;
-        const int c = __syncthreads_count(key >= up);
-        if (c >= K) {
+        const int n = __syncthreads_count(key >= up);
+        if (n >= K) {
             t = up;
-            if (c <= K + K / 4 + 2) break;
+            c = n;
         }
     }
-    return t;
+    return max(t, NONE);   // below it keys are no numbers'
 }
 
 }  // namespace bm

@@ -50,6 +50,26 @@ def test_beam_random(G, W, V, K, dtype, cuda_dev):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("K", [1, 4, 16])
+@pytest.mark.parametrize("V", [4, 9, 24, 40, 56, 72, 130, 700])
+def test_beam_values_of_both_signs(V, K, dtype, cuda_dev):
+    """Few places hold values, of both signs, large and tiny, so that the search for a
+    bound may end anywhere: also between the last negative value and none."""
+    G, W = 6, 2
+    logits, scores, g = _inputs(G, W, V, dtype, V + K)
+    runs = (torch.arange(V, device="cuda") // 8) % 2 * 2 - 1
+    logits[:2] = logits[:2].abs() * runs                           # runs of either sign
+    logits[2] = -logits[2].abs()
+    logits[3] = logits[3] * (10.0 ** torch.randint(-4, 4, (W, V), generator=g, device="cuda")).to(logits.dtype)
+    logits[4, :, V // 2:] = 0.0
+    logits[4, :, : V // 4] = -0.0
+    logits[5, 0] = -INF
+    logits[5, 0, V // 2] = -1e-3
+    scores[::2] = torch.tensor([5.0, -3.0], device="cuda")         # and totals of both signs
+    _check(logits, scores, K)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("V", [3001, 16400])
 def test_beam_masks_finished_and_dead(V, dtype, cuda_dev):
     """Masked tokens, masks that leave one token or none, the type's lowest value as a mask,

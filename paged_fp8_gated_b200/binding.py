@@ -559,10 +559,12 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
         out_dtype = dt if out is None else out.dtype
     if out_dtype is not dt and out_dtype is not torch.float32:
         raise TypeError(f"the result must be {dt} or float32, got {out_dtype}")
-    ldx = _rows(x, "x", dev, dt, (T, K))
+    ldx, one = x.stride()
+    if one != 1 and K > 1:
+        raise ValueError("x must have contiguous rows")
     ldw = _rows(w, "w", dev, dt, (N, K))
-    if T == 1:
-        ldx = -(-ldx // 8) * 8
+    if T == 1:     # a single row's stride is never followed
+        ldx = -(-K // 8) * 8
     if N == 1:
         ldw = -(-ldw // 8) * 8
     if bias is not None:

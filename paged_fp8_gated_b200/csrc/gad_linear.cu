@@ -6,7 +6,6 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
-#include <cmath>
 
 #include "gad_host.h"
 #include "gad_linear.cuh"
@@ -176,6 +175,8 @@ int narrow_tokens(int T) {
 // A chain of more than this many stages is promoted for a fp32 result.
 constexpr int kLongChain = 768 / gad::lin::BK;
 
+double larger(double a, double b) { return a > b ? a : b; }
+
 // The plan with the least time by this model of the kernels, in microseconds.
 // Its constants are fitted to every plan at T = 1 .. 2,048 over ten (K, N) from
 // 256 x 32,000 to 8,192 x 32,000, weights from memory, launches one behind
@@ -217,12 +218,13 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
                 if (promote && m > 1) continue;   // registers for two blocks
                 int stages = 1;
                 while (stages < own && stages < NARROW_MAX_STAGES && narrow_smem(tt, stages + 1) <= budget) ++stages;
-                auto wave = [&](double clusters) {
-                    const double blocks = clusters * c, per_sm = std::fmax(1.0, std::ceil(blocks / sms));
-                    double ts = std::fmax(0.294, per_sm * narrow_stage(tt) / 126e3);
-                    ts = std::fmax(ts, blocks * TILE / 5.9e6);
-                    if (own > stages) ts = std::fmax(ts, 1.48 / stages);
-                    const double shared = m == 1 ? std::fmax(per_sm, 1.6) : per_sm;
+                auto wave = [&](long long clusters) {
+                    const long long blocks = clusters * c;
+                    const double per_sm = static_cast<double>((blocks + sms - 1) / sms);
+                    double ts = larger(0.294, per_sm * narrow_stage(tt) / 126e3);
+                    ts = larger(ts, static_cast<double>(blocks * TILE) / 5.9e6);
+                    if (own > stages) ts = larger(ts, 1.48 / stages);
+                    const double shared = m == 1 ? larger(per_sm, 1.6) : per_sm;
                     return own * ts + 1.07 + 0.073 * c + tt * (0.0064 + 0.0206 * shared / c + 0.0029 * c);
                 };
                 const long long fit = cap.narrow[m][k], full = tiles / fit, rest = tiles % fit;
@@ -231,7 +233,7 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
                 q.split = c;
                 q.cls = m;
                 q.promote = promote;
-                q.us = start[m] + full * wave(static_cast<double>(fit)) + (rest ? wave(static_cast<double>(rest)) : 0.0);
+                q.us = start[m] + (full ? full * wave(fit) : 0.0) + (rest ? wave(rest) : 0.0);
                 if (promote) q.us *= 1.17;
                 take(q);
             }
@@ -239,7 +241,7 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
     }
     const double stage256 = T <= 256 ? 0.397 : 0.373;
     for (int bn = 256; bn >= 128; bn /= 2) {
-        const double tiles = std::ceil(T / 256.0) * std::ceil(static_cast<double>(N) / bn);
+        const long long tiles = static_cast<long long>((T + 255) / 256) * ((N + bn - 1) / bn);
         for (int k = 0; k < 3 && (1 << k) <= nk; ++k) {
             const int own = (nk + (1 << k) - 1) >> k;
             const bool promote = f32 && own > kLongChain;
@@ -251,13 +253,13 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
             q.bn = bn;
             q.split = 1 << k;
             q.promote = promote;
-            const double waves = std::ceil(tiles / cap.wide[k]);
+            const double waves = static_cast<double>((tiles + cap.wide[k] - 1) / cap.wide[k]);
             if (k == 0)
-                q.us = bn == 256 ? 4.4 + waves * std::fmax(own * stage256, 2.28) : 4.58 + waves * std::fmax(own * 0.2635, 1.4);
+                q.us = bn == 256 ? 4.4 + waves * larger(own * stage256, 2.28) : 4.58 + waves * larger(own * 0.2635, 1.4);
             else
                 q.us = 3.7 + 0.6 * (k == 2) + (bn == 256 ? own * stage256 + 2.9 : own * 0.2166 + 1.5);
             if (promote) q.us *= 1.1;
-            q.us = std::fmax(q.us, 1.9 + dram);
+            q.us = larger(q.us, 1.9 + dram);
             take(q);
         }
     }

@@ -170,6 +170,19 @@ def test_linear_forms(shape, cuda_dev):
     assert binding.linear_status() == 0
 
 
+@pytest.mark.parametrize("shape", [(3, 7, 5), (64, 1, 64), (5, 1001, 200), (260, 130, 2000), (300, 8193, 1000)], ids=str)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("fp16", "fp32")])
+def test_linear_what_lies_between_the_rows_is_not_read(shape, dtype, out, cuda_dev):
+    """K that ends inside 16 bytes, NaN behind it in both operands."""
+    from paged_fp8_gated_b200 import binding
+    T, K, N = shape
+    x, w, _, _ = _inputs(*shape, dtype, out, False, False, 17 + sum(shape))
+    ld = (K + 7) // 8 * 8 + 8
+    xs, ws = (torch.full((n, ld), float("nan"), device="cuda", dtype=x.dtype) for n in (T, N))
+    xs[:, :K], ws[:, :K] = x, w
+    _check(binding.linear(xs[:, :K], ws[:, :K], out_dtype=DT[out]), x, w)
+
+
 # pairs' tiles that end inside y's rows and columns: 256 and 128 columns, alone and two
 # or four pairs that share a tile
 EDGES = [(1300, 136, 2049), (300, 328, 9001), (193, 2056, 8203), (129, 1032, 8201), (450, 1032, 2001),
@@ -271,3 +284,32 @@ def test_linear_offsets_past_32_bits(T, N, cuda_dev):
     y.copy_(r)
     binding.linear(x, w, bias=b, residual=y, out=y)
     assert torch.equal(y, binding.linear(x, w, bias=b, residual=r))
+    binding.linear(x, w, bias=b, out=y)   # (by another way where rows are whole 16 bytes)
+    assert torch.equal(y, binding.linear(x, w, bias=b))
+
+
+@pytest.mark.parametrize("T,D", [(300, 512), (1024, 512), (700, 2048)])
+def test_linear_many_tokens_read_what_the_call_before_left(T, D, cuda_dev):
+    """The same with pairs' tiles, whose y leaves by TMA: a call reads the y of the one
+    before it, which may still run when it starts, and adds to it in place."""
+    from paged_fp8_gated_b200 import binding
+    x, w, b, _ = _inputs(T, D, D, "bf16", "bf16", True, False, 43)
+
+    def chain(wait):
+        a, every = x, []
+        for i in range(8):
+            a = binding.linear(a, w, bias=b, activation="silu")
+            if wait:
+                torch.cuda.synchronize()
+            every.append(a.clone())
+            binding.linear(every[-1], w, residual=a, out=a)
+            if wait:
+                torch.cuda.synchronize()
+            a = a / a.abs().max()
+            every.append(a)
+        return every
+    want = chain(True)
+    for _ in range(5):
+        got = chain(False)
+        torch.cuda.synchronize()
+        assert all(bool(p.isfinite().all()) and torch.equal(p, q) for p, q in zip(got, want))

@@ -180,7 +180,7 @@ double larger(double a, double b) { return a > b ? a : b; }
 // The plan with the least time by this model of the kernels, in microseconds.
 // Its constants are fitted to every plan at T = 1 .. 2,048 over ten (K, N) from
 // 256 x 32,000 to 8,192 x 32,000, weights from memory, launches one behind
-// another; the plan taken is there 0.7% slower than the fastest on average, 9% at
+// another; the plan taken is there 0.7% slower than the fastest on average, 11% at
 // most:
 //   narrow: a stage takes a block 0.294 (an SM draws 56 GB/s of weights), or its
 //     bytes at an SM's 126 GB/s from L2, or all blocks' weights at 5.9 TB/s, or
@@ -274,6 +274,10 @@ int launch_narrow(gad::lin::Params p, const void* x, long long ldx, const void* 
     p.tt = narrow_tokens(p.T);
     const int token_tiles = (p.T + p.tt - 1) / p.tt, nk = (p.K + BK - 1) / BK;
     const int budget = smem_share(512 >> plan.cls), own = (nk + plan.split - 1) / plan.split;
+    // Small blocks find room beside those of the launch before: weights asked for
+    // then 1 x 1,024 x 8,192 6.35 -> 5.95 us, 16 x 1,024 x 8,192 6.85 -> 6.25; in
+    // larger blocks, which start late, 1 x 8,192 x 2,304 9.9 -> 11.2.
+    p.early = plan.cls == 2;
     p.nstg = 1;
     while (p.nstg < NARROW_MAX_STAGES && p.nstg < own && narrow_smem(p.tt, p.nstg + 1) <= budget) ++p.nstg;
     if (narrow_smem(p.tt, p.nstg) > budget || narrow_cols(p.tt) * (ACC ? 2 : 1) > 512 >> plan.cls)

@@ -78,6 +78,7 @@ struct Params {
     int vec;                 // y (and residual) take aligned stores of four values
     int vec16;               // and of 16 bytes
     int tt, nstg;            // narrow: tokens per tile, ring stages
+    int early;               // narrow: the blocks start while the launch before runs
     int mt, nt;              // wide: tiles along the tokens and along N
     int by_tma;              // wide: y leaves by TMA (rows of whole 16 bytes of 16-bit values, no residual)
     int* err;                // status word: STATUS_LINEAR_WAIT when a bounded wait gave up
@@ -352,6 +353,12 @@ __device__ __forceinline__ void tma2_load_2d(uint32_t dst, const void* tmap, int
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
+// Brings a tile into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_map(const void* tmap) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }
@@ -607,7 +614,7 @@ namespace lin {
 // are in flight at a time: those from other blocks take about 500 cycles.
 template <int S, int THREADS>
 __device__ __forceinline__ void narrow_finish(const Params& p, uint32_t red, int rank, int n0, int t0, int tn) {
-    constexpr int U = S >= 8 ? 1 : S >= 4 ? 2 : 4;
+    constexpr int U = S >= 4 ? 1 : S == 2 ? 2 : 4;
     uint32_t base[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) base[s] = in_block(red, s);
@@ -713,6 +720,10 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS<ACC>, ACC == 0 ? 4 : ACC =
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
+    // the first weights into L2 while the launch before still runs (it may write
+    // them: L2 is where both meet)
+    if (p.early && tid == 0)
+        for (int kc = 0; kc < nk && kc < NSTG; ++kc) tma_prefetch_2d(&w_map, (k_first + kc) * BK, n0);
     pdl_wait_primary();
 
     if (warp == 0) {

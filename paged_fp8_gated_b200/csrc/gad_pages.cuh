@@ -207,20 +207,23 @@ __device__ __forceinline__ Small look_small(const Pool& p, int block) {
     s.rank = block_scan<SMALL_THREADS>(__popc(s.bits), &s.sum);
     return s;
 }
-// What every block of the cluster has in `mine`, added up: over the blocks
-// before this one (x), over all of them (y).  The cluster's threads pass two
-// barriers here.
+// What every block of the cluster has in `mine` (one value in all its threads),
+// added up: over the blocks before this one (x), over all of them (y).  Each
+// block stores its own in all of them, so one barrier does: behind it a block
+// reads its own memory only.  Call I = 0, 1, ... of the kernel has places of its
+// own; the first needs cluster_begin at the kernel's start, so that every block
+// is there to be stored to.
+__device__ __forceinline__ void cluster_begin() { cooperative_groups::this_cluster().barrier_arrive(); }
+template <int I>
 __device__ __forceinline__ uint2 cluster_sum(unsigned mine, int block) {
-    __shared__ unsigned s_sum;
+    __shared__ unsigned s_sums[SMALL_BLOCKS];
     const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
-    if (threadIdx.x == 0) s_sum = mine;
+    if (I == 0) cluster.barrier_wait();
+    if (threadIdx.x < SMALL_BLOCKS) *cluster.map_shared_rank(&s_sums[block], threadIdx.x) = mine;
     cluster.sync();
     const int lane = threadIdx.x & 31;
-    const unsigned v = lane < SMALL_BLOCKS ? *cluster.map_shared_rank(&s_sum, lane) : 0;
-    const uint2 r = make_uint2(__reduce_add_sync(0xffffffffu, lane < block ? v : 0),
-                               __reduce_add_sync(0xffffffffu, v));
-    cluster.sync();   // everyone has read it: it may change, and the block may end
-    return r;
+    const unsigned v = lane < SMALL_BLOCKS ? s_sums[lane] : 0;
+    return make_uint2(__reduce_add_sync(0xffffffffu, lane < block ? v : 0), __reduce_add_sync(0xffffffffu, v));
 }
 
 }  // namespace pg
@@ -246,7 +249,7 @@ struct ForkParams {
 // have in common in a column, and a count is touched only if something is left.
 // Tables that leave the GPU with few blocks take one column a thread (U = 1),
 // larger ones four, as vectors if the rows allow it (VEC).
-// 128 new rows of 30,000 single-token pages (38 MB) 8.6 us, 64 of 940 pages 7.7;
+// 128 new rows of 30,000 single-token pages (38 MB) 8.6 us, 64 of 940 pages 7.4;
 // the counts' atomics, one for a page that several rows share, are its slow part.
 template <int U, bool VEC>
 __global__ void __launch_bounds__(pg::THREADS) fork_kernel(const ForkParams p) {
@@ -421,9 +424,10 @@ __global__ void __cluster_dims__(pg::SMALL_BLOCKS, 1, 1) __launch_bounds__(pg::S
     __shared__ int s_rows[MAX_ROWS];
     const int block = blockIdx.x;
     pdl_wait_primary();
+    cluster_begin();
     const Small s = look_small(p.pool, block);
     const int need = fork_list<SMALL_THREADS>(p, s_rows);   // in every block
-    const uint2 f = cluster_sum(s.sum, block);
+    const uint2 f = cluster_sum<0>(s.sum, block);
     const int before = static_cast<int>(f.x), total = static_cast<int>(f.y);
     if (block == 0 && total < need) fork_short<SMALL_THREADS>(p, s_rows, total, need, pool_bit);
     hand_out<SMALL_THREADS>(s.bits, s.mine, s.rank, min(s.sum, need - before), before,
@@ -574,13 +578,14 @@ __global__ void __cluster_dims__(pg::SMALL_BLOCKS, 1, 1) __launch_bounds__(pg::S
     using namespace pg;
     __shared__ int s_prefix[MAX_ROWS], s_len[MAX_ROWS];
     const int tid = threadIdx.x, block = blockIdx.x;
+    cluster_begin();
     const Small s = look_small(p.pool, block);
     bool over;
     const int need = extend_rows<SMALL_THREADS>(p, &over, [&](int r, int len, int before) {   // in every block
         s_len[r] = len;
         s_prefix[r] = before;
     });
-    const uint2 f = cluster_sum(s.sum, block);   // and every block has read the lengths
+    const uint2 f = cluster_sum<0>(s.sum, block);   // and every block has read the lengths
     const int before = static_cast<int>(f.x);
     const bool enough = need <= static_cast<int>(f.y), ok = !over && enough;
     if (block == 0 && tid == 0) p.ws.head->status = (over ? row_bit : 0) | (enough ? 0 : pool_bit);
@@ -614,8 +619,7 @@ __global__ void free_kernel(const FreeParams p) {
     const int r = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
     if (p.leave != nullptr && p.leave[r] == 0) return;   // the whole cluster
     const int n = pages_of(p.lens[r], p.shift, p.max_pages);
-    cooperative_groups::this_cluster().sync();
-    if (part == 0 && threadIdx.x == 0) p.lens[r] = -1;
+    cooperative_groups::this_cluster().barrier_arrive();   // the length has been read
     const int* row = p.table + static_cast<size_t>(r) * p.max_pages;
     const long long stride = static_cast<long long>(p.parts) * blockDim.x;
     for (long long j0 = static_cast<long long>(part) * blockDim.x + threadIdx.x; j0 < n; j0 += 4 * stride) {
@@ -626,6 +630,8 @@ __global__ void free_kernel(const FreeParams p) {
         for (int u = 0; u < 4; ++u)
             if (page[u] >= 0 && page[u] < p.num_pages) atomicAdd(p.refs + page[u], -1);
     }
+    cooperative_groups::this_cluster().barrier_wait();
+    if (part == 0 && threadIdx.x == 0) p.lens[r] = -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -642,7 +648,7 @@ struct CompactParams {
 };
 
 // compact: 2^20 pages in three launches 18 us, half of it for the tables and counts
-// (two dependent loads an entry); 16,384 in two launches 10.
+// (two dependent loads an entry); 16,384 in two launches 9.4.
 __global__ void __launch_bounds__(pg::THREADS) compact_count_kernel(const CompactParams p) {
     using namespace pg;
     pdl_launch_dependents();
@@ -737,13 +743,14 @@ __global__ void __cluster_dims__(pg::SMALL_BLOCKS, 1, 1) __launch_bounds__(pg::S
     using namespace pg;
     const int tid = threadIdx.x, block = blockIdx.x;
     pdl_launch_dependents();
+    cluster_begin();
     const Small s = look_small(p.pool, block);
-    const uint2 f = cluster_sum(s.sum, block);
+    const uint2 f = cluster_sum<0>(s.sum, block);
     const int total = static_cast<int>(p.pool.num_pages - f.y);
     const int below = total - s.mine;   // the thread's pages below `total`
     const unsigned low = below >= RUN ? s.bits : below > 0 ? s.bits & ((1u << below) - 1) : 0;
     const unsigned mine = block_sum2<SMALL_THREADS>(__popc(low), 0).x;
-    const Moves m = compact_moves(p, total, cluster_sum(mine, block).y);
+    const Moves m = compact_moves(p, total, cluster_sum<1>(mine, block).y);
     if (block == 0 && tid == 0) compact_head(p, m);
     for (long long k = m.moves + block * SMALL_THREADS + tid; k < p.max_moves; k += SMALL_BLOCKS * SMALL_THREADS)
         p.copy_src[k] = p.copy_dst[k] = -1;

@@ -58,12 +58,6 @@ constexpr int ROWS = 128;                    // weight rows (narrow), tokens or 
 constexpr int TILE = ROWS * BK * 2;          // bytes of 128 rows of a stage
 constexpr int SEG = 512 / BK;                // stages of a chain that is promoted
 
-// Limit of the waits for a block's own copies and MMAs before it leaves.  Not the
-// pipeline waits' value, by which the build that gives up at the first miss tells
-// those: a block that left with copies in flight to it would fault.
-constexpr unsigned long long LAST_LIMIT_NS = TEARDOWN_LIMIT_NS + 1;
-static_assert(LAST_LIMIT_NS != WAIT_LIMIT_NS, "never given up at the first miss");
-
 enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
 enum Out { OUT_BF16 = 0, OUT_F16 = 1, OUT_F32 = 2 };
 
@@ -740,7 +734,7 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS<ACC>, ACC == 0 ? 4 : ACC =
             }
             // every load has landed before the shared memory is used again
             for (int kc = issued > NSTG ? issued - NSTG : 0; kc < issued; ++kc)
-                wait_bounded(FULL(kc % NSTG), (kc / NSTG) & 1, abort_flag, false, LAST_LIMIT_NS);
+                wait_bounded(FULL(kc % NSTG), (kc / NSTG) & 1, abort_flag, false, TEARDOWN_LIMIT_NS);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -794,7 +788,7 @@ __global__ void __launch_bounds__(lin::NARROW_THREADS<ACC>, ACC == 0 ? 4 : ACC =
             if (lane == 0) mbar_arrive(CEMPTY(c & 1));
         }
     }
-    const bool done = wait_bounded(DONE, 0, abort_flag, false, LAST_LIMIT_NS);
+    const bool done = wait_bounded(DONE, 0, abort_flag, false, TEARDOWN_LIMIT_NS);
     tc_fence_after();
     __syncthreads();   // the loads have landed (warp 0) and the MMAs are done: the ring is free
 
@@ -1036,7 +1030,7 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
     }
     // ---- teardown: the MMAs are done (both blocks see it), then tensor memory goes ----
     // (one warp asks; the others would take its issue slots from the epilogue)
-    if (warp == 1) wait_bounded(DONE, 0, abort_flag, false, LAST_LIMIT_NS);
+    if (warp == 1) wait_bounded(DONE, 0, abort_flag, false, TEARDOWN_LIMIT_NS);
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
@@ -1089,7 +1083,7 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
             for (int i = last > STAGES ? last - STAGES : 0; i < last; ++i) {
                 if (i >= theirs) mbar_complete_tx(FULL(i % STAGES), STAGE);
                 else if (i >= mine) mbar_arrive_expect_tx(FULL(i % STAGES), STAGE);
-                wait_bounded(FULL(i % STAGES), (i / STAGES) & 1, abort_flag, false, LAST_LIMIT_NS);
+                wait_bounded(FULL(i % STAGES), (i / STAGES) & 1, abort_flag, false, TEARDOWN_LIMIT_NS);
             }
         }
         __syncthreads();
@@ -1109,7 +1103,7 @@ __global__ void __launch_bounds__(lin::WIDE_THREADS, 1)
                                       in_block(RECEIVED, 2 * d + rank));
             }
             __syncwarp();
-            const bool got = wait_bounded(RECEIVED, 0, abort_flag, false, LAST_LIMIT_NS);
+            const bool got = wait_bounded(RECEIVED, 0, abort_flag, false, TEARDOWN_LIMIT_NS);
             tc_fence_after();
             if (__all_sync(0xffffffffu, got && !gave_up)) {
                 const int first = part * (BN / S);

@@ -72,7 +72,10 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 // the last waits of a kernel (for its own tensor-core operations and copies in
 // flight, before it frees tensor memory and exits) use TEARDOWN_LIMIT_NS.
 constexpr unsigned long long WAIT_LIMIT_NS = 2000000000ull;
-constexpr unsigned long long TEARDOWN_LIMIT_NS = 2000000000ull;
+constexpr unsigned long long TEARDOWN_LIMIT_NS = 2000000001ull;
+// (The build that gives up at the first miss tells the two by their values: a block
+// that left with copies or MMAs in flight could fault.)
+static_assert(TEARDOWN_LIMIT_NS != WAIT_LIMIT_NS, "the last waits are waited for in every build");
 
 // The library built for the tests of the give-up path (and only that build)
 // defines GAD_TEST_GIVE_UP_AT_FIRST_MISS: there a pipeline wait whose phase has

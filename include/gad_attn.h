@@ -481,7 +481,10 @@ int gad_linear_status(int* status, void* stream);
  *               calls that overlap on the GPU need different ones
  *
  * Scores are compared in 64 bits and rounded to float32 on output; equal
- * scores go to the lower w * V + v.  (A beam offers its K largest logits, ties to
+ * scores go to the lower w * V + v.  The log-sums behind them are of exponentials
+ * in 32 bits: off by at most 7e-6 at any V, usually by 1e-7, so two beams'
+ * candidates that are closer may come in either order (beams with equal rows have
+ * equal log-sums).  (A beam offers its K largest logits, ties to
  * the lower token: beside a score above about 1e9 in magnitude, where 64 bits
  * no longer tell its logits apart, that is the order that counts.)  A logit of
  * -infinity or NaN is never chosen; a beam whose logits hold a NaN or +infinity

@@ -41,7 +41,7 @@ BeamWs beam_ws(long long rows, int V, int K) {
     w.cand_off = off;
     off = align_up(off + parts * K * sizeof(uint64_t));
     w.sum_off = off;
-    off = align_up(off + parts * sizeof(float2));
+    off = align_up(off + parts * sizeof(gad::bm::Sum));
     w.total = off;
     return w;
 }
@@ -110,7 +110,7 @@ int gad_beam_select(const void* logits, int dtype, int64_t row_stride, const flo
     p.NV = cut.NV;
     p.pad = pad_token;
     p.cand = reinterpret_cast<uint64_t*>(ws + w.cand_off);
-    p.sums = reinterpret_cast<float2*>(ws + w.sum_off);
+    p.sums = reinterpret_cast<gad::bm::Sum*>(ws + w.sum_off);
     p.out_scores = out_scores;
     p.out_parent = out_parent;
     p.out_token = out_token;

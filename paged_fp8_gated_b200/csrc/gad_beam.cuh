@@ -11,10 +11,22 @@
 // suffices: each block takes a segment of a row and leaves its K best logits,
 // its maximum m and its sum of exp(x - m) (beam_chunk_kernel); a second kernel
 // joins the segments' sums into lse_w and ranks the W S K candidates
-// (beam_merge_kernel).  The scores that decide the order are held in 64 bits:
-// candidates of different beams can be as close as the last bits of lse_w.  A
-// row's elements go to threads by their index, whatever the row's alignment,
-// so equal rows have equal sums and tie exactly.
+// (beam_merge_kernel).  The scores that decide the order are held in 64 bits, and
+// all sums in 64 bits or two words of 32, but those of the at most 32 exponentials
+// that a thread adds up at a time: lse_w is as good as the exponentials, however long the row.  Those are of
+// fp32 differences d scaled by log2 e, each off by at most 2.5 2^-24 |d| (the
+// difference's rounding, the product's and the constant's) + 2^-22 (the function)
+// + 2^-24 (a product with it) of itself.  A thread's terms are relative to a reference that moves only when the
+// maximum passes it by FAR, so a term is scaled once for its own difference, once
+// for every FAR that the maximum rises behind it, and once to the segment's maximum.
+// With the weights p_v = exp(x_v - lse) the sum of p times the distance to the row's
+// maximum is at most log V, so lse_w is off by at most
+//
+//   2^-24 (2.5 (log V + 2 FAR) + 5 (2 + log V / FAR) + 18),
+//
+// 6.6e-6 at V = 2^24, and in practice by 1e-7 (the terms' errors differ in sign).  A
+// row's elements go to threads by their index, whatever the row's alignment, so
+// equal rows have equal sums and tie exactly.
 //
 // The K best of a segment: every thread streams its elements through registers
 // for its maximum and sum only, without a barrier.  The K-th largest of the
@@ -50,6 +62,7 @@ constexpr int MERGE_BUF = 1024; // a request's
 constexpr int GROUP = 4;        // vectors of a thread in flight
 constexpr float NEG_INF = -__builtin_huge_valf();
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr float FAR = 4.f;      // how far a maximum may pass the sum's reference
 
 // A word of two 16-bit elements of which `left` belong to the row.
 __device__ __forceinline__ uint32_t cut16(uint32_t w, int left, uint32_t lowest) {
@@ -186,6 +199,13 @@ __device__ __forceinline__ uint32_t kth_key(uint32_t key, int K) {
 
 }  // namespace bm
 
+namespace bm {
+struct Sum {
+    double sum;   // of exp(x - top)
+    float top;    // the maximum
+};
+}  // namespace bm
+
 struct BeamParams {
     const void* logits;
     long long ld;             // elements from one row of logits to the next
@@ -195,7 +215,7 @@ struct BeamParams {
     int S, NV;                // S segments per row, of NV vectors per thread
     int pad;
     uint64_t* cand;           // [G W S K] the segments' best logits and their tokens, best first (see pack)
-    float2* sums;             // [G W S] maximum, sum of exp(x - maximum)
+    bm::Sum* sums;            // [G W S]
     float* out_scores;
     int *out_parent, *out_token;
 };
@@ -284,7 +304,8 @@ __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamPa
     // ---- maximum and sum of exponentials (a NaN or +inf makes the sum NaN) ----
     uint32_t raw[GROUP][4], next[GROUP][4];
     load(next, 0);
-    float m = NEG_INF, sum = 0.f;
+    float m = NEG_INF, ref = NEG_INF;   // maximum; what the sum's terms are relative to
+    float sum = 0.f, low = 0.f;         // of exp(x - ref): sum + low
     for (int i0 = 0; i0 < p.NV; i0 += GROUP) {
 #pragma unroll
         for (int i = 0; i < GROUP; ++i)
@@ -296,21 +317,28 @@ __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamPa
         for (int i = 0; i < GROUP; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) wm = E::word_max(wm, raw[i][j]);
-        const float mine = E::top(wm);
-        if (mine > m) {
-            sum *= fast_exp2((m - mine) * LOG2E);
-            m = mine;
+        m = fmaxf(m, E::top(wm));
+        if (m > ref + FAR) {
+            const float f = fast_exp2((ref - m) * LOG2E);
+            sum *= f;
+            low *= f;
+            ref = m;
         }
-        const float ref = m > NEG_INF ? m : 0.f;
+        const float r = ref > NEG_INF ? ref : 0.f;
         float2 part = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < GROUP; ++i)
 #pragma unroll
             for (int q = 0; q < VEC / 2; ++q) {
-                const float2 d = mul2(add2(E::pair(raw[i], q), make_float2(-ref, -ref)), make_float2(LOG2E, LOG2E));
+                const float2 d = mul2(add2(E::pair(raw[i], q), make_float2(-r, -r)), make_float2(LOG2E, LOG2E));
                 part = add2(part, make_float2(fast_exp2(d.x), fast_exp2(d.y)));
             }
-        sum += part.x + part.y;
+        // the sum's rounding is kept in `low`: exactly, but where `more` is larger than all
+        // before it, which doubles the sum and so happens for 2 2^-24 of it at most.  (A
+        // sum in double took longer, on the exponentials' unit, which converts.)
+        const float more = part.x + part.y, both = sum + more;
+        low += more - (both - sum);
+        sum = both;
     }
 
     // ---- the segment's maximum and sum ----
@@ -321,7 +349,8 @@ __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamPa
     const float thr = from_key(kth_key(order_key(m), p.K));   // its barriers cover s_m and s_n
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, s_m[w]);
-    double total = m == top ? sum : sum * fast_exp2((m - top) * LOG2E);   // equal infinities have no difference
+    double total = static_cast<double>(sum) + low;
+    if (ref != top) total *= fast_exp2((ref - top) * LOG2E);   // equal infinities have no difference
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
     if (lane == 0) s_sum[tid >> 5] = total;
@@ -367,7 +396,7 @@ __global__ void __launch_bounds__(bm::THREADS, 4) beam_chunk_kernel(const BeamPa
         total = lane < THREADS / 32 ? s_sum[lane] : 0.0;
 #pragma unroll
         for (int d = THREADS / 64; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        if (lane == 0) p.sums[part] = make_float2(top, static_cast<float>(total));
+        if (lane == 0) p.sums[part] = {total, top};
     }
     uint64_t* out = p.cand + part * p.K;
     const int n = s_n;
@@ -432,22 +461,21 @@ __global__ void __launch_bounds__(bm::THREADS) beam_merge_kernel(const BeamParam
     if (tid == 0) s_n = 0;
     for (int w = tid >> 5; w < p.W; w += THREADS / 32) {
         const int row = g * p.W + w;
-        const float2* ms = p.sums + static_cast<size_t>(row) * p.S;
-        const float2 mine = lane < p.S ? ms[lane] : make_float2(NEG_INF, 0.f);   // not written for some rows
+        const Sum* ms = p.sums + static_cast<size_t>(row) * p.S;
+        const Sum mine = lane < p.S ? ms[lane] : Sum{0.0, NEG_INF};   // not written for some rows
         const float cum = p.scores[row];
         const bool done = p.finished != nullptr && p.finished[row] != 0;
         double lse = 0;
         if (!done && isfinite(cum)) {
-            float m = fmaxf(mine.x, NEG_INF);
-            for (int s = lane + 32; s < p.S; s += 32) m = fmaxf(m, ms[s].x);
+            float m = fmaxf(mine.top, NEG_INF);
+            for (int s = lane + 32; s < p.S; s += 32) m = fmaxf(m, ms[s].top);
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
             double sum = 0;
             for (int s = lane; s < p.S; s += 32) {
-                const float2 q = s == lane ? mine : ms[s];
+                const Sum q = s == lane ? mine : ms[s];
                 // a segment without a finite logit adds nothing, unless it holds a NaN
-                sum += q.x > NEG_INF ? q.y * exp(static_cast<double>(q.x) - m)
-                                     : static_cast<double>(q.y != q.y ? q.y : 0.f);
+                sum += q.top > NEG_INF ? q.sum * exp(static_cast<double>(q.top) - m) : q.sum != q.sum ? q.sum : 0.0;
             }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);

@@ -489,7 +489,8 @@ int gad_linear_status(int* status, void* stream);
  * no longer tell its logits apart, that is the order that counts.)  A logit of
  * -infinity or NaN is never chosen; a beam whose logits hold a NaN or +infinity
  * has no log-sum and thus no candidates.  Places that no candidate fills get score -infinity and
- * parent and token -1.  Outputs may not overlap scores (GAD_ERR_UNSUPPORTED).
+ * parent and token -1.  Outputs and workspace may not overlap scores, finished or
+ * one another, nor the workspace logits (GAD_ERR_UNSUPPORTED).
  * Asynchronous on `stream`, allocates nothing, graph-capturable.
  */
 int gad_beam_select(const void* logits, int dtype, int64_t row_stride, const float* scores, const uint8_t* finished,

@@ -79,16 +79,21 @@ int gad_beam_select(const void* logits, int dtype, int64_t row_stride, const flo
     if (!aligned(logits, dtype == GAD_DTYPE_F32 ? 4 : 2) || !aligned(scores, 4) || !aligned(out_scores, 4) ||
         !aligned(out_parent, 4) || !aligned(out_token, 4))
         return fail(GAD_ERR_ALIGN, "every array must be aligned to its element size");
-    const size_t in = static_cast<size_t>(G) * W * 4, out = static_cast<size_t>(G) * K * 4;
-    for (const void* o : {static_cast<const void*>(out_scores), static_cast<const void*>(out_parent),
-                          static_cast<const void*>(out_token)})
-        if (overlap(scores, in, o, out)) return fail(GAD_ERR_UNSUPPORTED, "the outputs may not overlap scores");
     if (!workspace) return fail(GAD_ERR_WORKSPACE, "workspace is NULL");
     if (!aligned(workspace, kAlign)) return fail(GAD_ERR_ALIGN, "workspace must be 256-byte aligned");
     const long long rows = static_cast<long long>(G) * W;
     const BeamWs w = beam_ws(rows, V, K);
     if (workspace_bytes < w.total)
         return fail(GAD_ERR_WORKSPACE, "workspace %zu B < required %zu B", workspace_bytes, w.total);
+    // (a request's results are written while other requests' scores and marks are still
+    // read, but behind the last read of the logits)
+    const size_t in = static_cast<size_t>(rows), out = static_cast<size_t>(G) * K * 4;
+    const size_t all = ((rows - 1) * static_cast<size_t>(row_stride) + V) * (dtype == GAD_DTYPE_F32 ? 4 : 2);
+    if (written_overlap({{out_scores, out}, {out_parent, out}, {out_token, out}, {workspace, w.total}},
+                        {{scores, in * 4}, {finished, in}}) ||
+        overlap(workspace, w.total, logits, all))
+        return fail(GAD_ERR_UNSUPPORTED, "outputs and workspace may not overlap scores, finished or one another, "
+                                         "nor the workspace logits");
     int sms = 0, major = 0;
     st = current_device_sms(&sms, &major);
     if (st != GAD_OK) return st;

@@ -10,6 +10,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include "gad_attn.h"
 #include "gad_error.h"
@@ -34,10 +35,27 @@ inline int current_device_sms(int* sms, int* major) {
     return GAD_OK;
 }
 
-// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
+// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte (a NULL one, of an
+// argument that is left out, shares none).
 inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
+    return x != 0 && y != 0 && x < y + nb && y < x + na;
+}
+
+// A stretch of memory that a call reads or writes.
+struct Span {
+    const void* p;
+    size_t n;
+};
+// Whether a stretch that is written shares a byte with another one of the call.
+inline bool written_overlap(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+    for (const Span* w = written.begin(); w != written.end(); ++w) {
+        for (const Span* o = w + 1; o != written.end(); ++o)
+            if (overlap(w->p, w->n, o->p, o->n)) return true;
+        for (const Span& r : read)
+            if (overlap(w->p, w->n, r.p, r.n)) return true;
+    }
+    return false;
 }
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

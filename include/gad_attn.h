@@ -524,8 +524,9 @@ size_t gad_beam_workspace_bytes(int G, int W, int V, int K);
  * follow from the inputs alone.  Page ids outside [0, num_pages) are never
  * followed.  page_size is 1 or 64, rows 1 to GAD_MAX_B.
  *
- * Calls run asynchronously on `stream`, allocate nothing and can be captured.
- * The workspace (gad_pages_workspace_bytes, 256-byte aligned) needs no initial
+ * Calls run asynchronously on `stream`, allocate nothing and can be captured.  An
+ * array that a call writes may not overlap another one of that call, the
+ * workspace included (GAD_ERR_UNSUPPORTED).  The workspace (gad_pages_workspace_bytes, 256-byte aligned) needs no initial
  * contents; calls that overlap on the GPU, or that share a pool, must not run
  * at the same time.  Its first word is the call's status: GAD_STATUS_PAGES_*
  * bits, read with gad_attn_step_status.
@@ -556,8 +557,7 @@ int gad_pages_copy(void* const* caches, int n_caches, size_t page_bytes, int64_t
  * page_size) and GAD_STATUS_PAGES_POOL is set.
  *
  *   parent      int32 [rows_out]
- *   out_table   int32 [rows_out, max_pages], out_lens int32 [rows_out]; they may
- *               not overlap page_table and lens (GAD_ERR_UNSUPPORTED)
+ *   out_table   int32 [rows_out, max_pages]; out_lens int32 [rows_out]
  *   copy_src,   int32 [rows_out]
  *   copy_dst
  */

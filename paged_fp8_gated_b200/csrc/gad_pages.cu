@@ -77,6 +77,17 @@ int check_ws(const void* workspace, size_t bytes, int64_t num_pages) {
     return GAD_OK;
 }
 
+// A table of `rows` rows, in bytes.
+size_t table_bytes(int rows, int max_pages) { return static_cast<size_t>(rows) * max_pages * 4; }
+size_t row_bytes(int rows) { return static_cast<size_t>(rows) * 4; }
+
+// Blocks read and write a call's arrays at the same time.
+int check_overlap(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+    if (written_overlap(written, read))
+        return fail(GAD_ERR_UNSUPPORTED, "an array that the call writes may not overlap another one of the call");
+    return GAD_OK;
+}
+
 int check_device() {
     int sms = 0, major = 0;
     const int st = current_device_sms(&sms, &major);
@@ -142,7 +153,10 @@ int gad_pages_copy(void* const* caches, int n_caches, size_t page_bytes, int64_t
         if (!aligned(caches[i], 16)) return fail(GAD_ERR_ALIGN, "caches[%d] must be 16-byte aligned", i);
     }
     if (!aligned(src, 4) || !aligned(dst, 4)) return fail(GAD_ERR_ALIGN, "src and dst must be 4-byte aligned");
-    int st = check_device();
+    int st = GAD_OK;
+    for (int i = 0; i < n_caches && n > 0 && st == GAD_OK; ++i)
+        st = check_overlap({{caches[i], num_pages * page_bytes}}, {{src, row_bytes(n)}, {dst, row_bytes(n)}});
+    if (st == GAD_OK) st = check_device();
     if (st != GAD_OK || n == 0) return st;
 
     gad::CopyParams p;
@@ -187,11 +201,16 @@ int gad_pages_fork(const int32_t* page_table, const int32_t* lens, int rows_in, 
                           static_cast<const void*>(out_lens), static_cast<const void*>(copy_src),
                           static_cast<const void*>(copy_dst)})
         if (!aligned(q, 4)) return fail(GAD_ERR_ALIGN, "tables, lengths, parent and copy lists need 4-byte alignment");
-    const size_t row_bytes = static_cast<size_t>(max_pages) * 4;
-    if (overlap(page_table, rows_in * row_bytes, out_table, rows_out * row_bytes) ||
-        overlap(lens, static_cast<size_t>(rows_in) * 4, out_lens, static_cast<size_t>(rows_out) * 4))
-        return fail(GAD_ERR_UNSUPPORTED, "the new tables and lengths may not overlap the old ones");
-    st = check_device();
+    st = check_overlap({{out_table, table_bytes(rows_out, max_pages)},
+                        {out_lens, row_bytes(rows_out)},
+                        {copy_src, row_bytes(rows_out)},
+                        {copy_dst, row_bytes(rows_out)},
+                        {refs, static_cast<size_t>(num_pages) * 4},
+                        {workspace, pages_ws(num_pages).total}},
+                       {{page_table, table_bytes(rows_in, max_pages)},
+                        {lens, row_bytes(rows_in)},
+                        {parent, row_bytes(rows_out)}});
+    if (st == GAD_OK) st = check_device();
     if (st != GAD_OK) return st;
 
     gad::ForkParams p;
@@ -241,7 +260,15 @@ int gad_pages_extend(int32_t* page_table, int32_t* lens, int rows, int L, int ma
     if (st != GAD_OK) return st;
     if (!aligned(positions, 8) || !aligned(cache_loc, 8) || !aligned(page_table, 4) || !aligned(lens, 4))
         return fail(GAD_ERR_ALIGN, "positions/cache_loc need 8-byte, page_table/lens 4-byte alignment");
-    st = check_device();
+    const size_t token_bytes = static_cast<size_t>(rows) * L * 8;
+    st = check_overlap({{page_table, table_bytes(rows, max_pages)},
+                        {lens, row_bytes(rows)},
+                        {refs, static_cast<size_t>(num_pages) * 4},
+                        {positions, token_bytes},
+                        {cache_loc, token_bytes},
+                        {workspace, pages_ws(num_pages).total}},
+                       {});
+    if (st == GAD_OK) st = check_device();
     if (st != GAD_OK) return st;
 
     gad::ExtendParams p;
@@ -279,7 +306,9 @@ int gad_pages_free(const int32_t* page_table, int32_t* lens, int rows, const uin
     if (st != GAD_OK) return st;
     if (!aligned(page_table, 4) || !aligned(lens, 4))
         return fail(GAD_ERR_ALIGN, "page_table and lens need 4-byte alignment");
-    st = check_device();
+    st = check_overlap({{lens, row_bytes(rows)}, {refs, static_cast<size_t>(num_pages) * 4}},
+                       {{page_table, table_bytes(rows, max_pages)}, {leave, static_cast<size_t>(rows)}});
+    if (st == GAD_OK) st = check_device();
     if (st != GAD_OK) return st;
     gad::FreeParams p;
     std::memset(&p, 0, sizeof(p));
@@ -338,7 +367,14 @@ int gad_pages_compact(int32_t* page_table, const int32_t* lens, int rows, int ma
     if (!aligned(page_table, 4) || !aligned(lens, 4) || !aligned(copy_src, 4) || !aligned(copy_dst, 4) ||
         !aligned(used, 4))
         return fail(GAD_ERR_ALIGN, "tables, lengths, copy lists and used need 4-byte alignment");
-    st = check_device();
+    st = check_overlap({{page_table, table_bytes(rows, max_pages)},
+                        {refs, static_cast<size_t>(num_pages) * 4},
+                        {copy_src, row_bytes(max_moves)},
+                        {copy_dst, row_bytes(max_moves)},
+                        {used, 4},
+                        {workspace, pages_ws(num_pages).total}},
+                       {{lens, row_bytes(rows)}});
+    if (st == GAD_OK) st = check_device();
     if (st != GAD_OK) return st;
     gad::CompactParams p;
     std::memset(&p, 0, sizeof(p));

@@ -438,7 +438,10 @@ typedef enum {
  *
  * Sums and the epilogue are held in fp32, y is rounded once.  y may be the
  * residual itself (same address and stride); any other overlap of y with the
- * inputs is refused (GAD_ERR_UNSUPPORTED).  Results do not depend on timing.
+ * inputs is refused (GAD_ERR_UNSUPPORTED).  Different columns of one wider matrix
+ * (rows the same number of bytes apart) are no overlap; between rows at different
+ * distances the whole stretch from a matrix's first value to its last one counts.
+ * Results do not depend on timing.
  * gad_oproj is the special case without an epilogue that chains to a step.
  * Asynchronous on `stream`, allocates nothing; make the first call on a device
  * before any stream capture on it.

@@ -60,8 +60,26 @@ int encode_tiles(CUtensorMap* map, const void* base, bool fp16, int cols, int ro
     return GAD_OK;
 }
 
-size_t extent(long long rows, long long ld, long long cols, int elem) {
-    return static_cast<size_t>((rows - 1) * ld + cols) * elem;
+// A matrix as its rows in memory, all in bytes.
+struct Rows {
+    const void* p;
+    size_t rows, ld, width;
+    Rows(const void* base, long long n, long long stride, long long cols, int elem)
+        : p(base), rows(static_cast<size_t>(n)), ld(static_cast<size_t>(stride) * elem),
+          width(static_cast<size_t>(cols) * elem) {}
+    size_t extent() const { return (rows - 1) * ld + width; }
+};
+// Whether a row of one shares a byte with a row of the other.  Rows at one distance
+// (a single row has any) lie side by side, as the columns of a wider matrix, where
+// b's place within a's distance leaves room for both; others share none only if the
+// matrices' whole extents do.
+bool rows_overlap(const Rows& a, const Rows& b) {
+    if (!overlap(a.p, a.extent(), b.p, b.extent())) return false;
+    const size_t ld = a.rows > 1 ? a.ld : b.ld;
+    if (b.rows > 1 && b.ld != ld) return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    const size_t at = y >= x ? (y - x) % ld : (ld - (x - y) % ld) % ld;
+    return at < a.width || at + b.width > ld;
 }
 
 // Shared memory: 228 KB per SM, 1 KB of it the system's per block, 227 KB per
@@ -365,11 +383,11 @@ int gad_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const voi
     if (!aligned(x, 16) || !aligned(w, 16)) return fail(GAD_ERR_ALIGN, "x and w must be 16-byte aligned");
     if (!aligned(bias, 2) || !aligned(y, oe) || !aligned(residual, oe))
         return fail(GAD_ERR_ALIGN, "bias, residual and y must be aligned to their element size");
-    const size_t ny = extent(T, ldy, N, oe);
-    if (overlap(y, ny, x, extent(T, ldx, K, 2)) || overlap(y, ny, w, extent(N, ldw, K, 2)) ||
-        (bias && overlap(y, ny, bias, static_cast<size_t>(N) * 2)))
+    const Rows out(y, T, ldy, N, oe);
+    if (rows_overlap(out, Rows(x, T, ldx, K, 2)) || rows_overlap(out, Rows(w, N, ldw, K, 2)) ||
+        (bias && rows_overlap(out, Rows(bias, 1, N, N, 2))))
         return fail(GAD_ERR_UNSUPPORTED, "y may not overlap x, w or bias");
-    if (residual && !(residual == y && ldr == ldy) && overlap(y, ny, residual, extent(T, ldr, N, oe)))
+    if (residual && !(residual == y && ldr == ldy) && rows_overlap(out, Rows(residual, T, ldr, N, oe)))
         return fail(GAD_ERR_UNSUPPORTED, "y may be residual itself, but not overlap it otherwise");
     int sms = 0, major = 0;
     int st = current_device_sms(&sms, &major);

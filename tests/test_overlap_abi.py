@@ -69,3 +69,22 @@ def test_pages_copy_lists_inside_a_cache_are_refused(B, which):
     lists = [3 * F, 4 * F]
     lists[which] = 2 * F + 64 * 128 - 4
     _refused(B, B.lib().gad_pages_copy(caches, 2, 128, 64, *lists, 4, None))
+
+
+def _linear(B, **o):
+    a = dict(x=F, ldx=256, w=2 * F, ldw=64, bias=None, residual=None, ldr=0, y=4 * F, ldy=256, T=4, K=64, N=100,
+             dtype=1, out=1, act=0)
+    a.update(o)
+    return B.lib().gad_linear(*a.values(), None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(y=F), dict(y=F + 126), dict(y=F - 198), dict(y=F + 3 * 512 + 126), dict(y=F - 3 * 512),   # x: 128 of 512 bytes
+    dict(y=F + 314), dict(y=F + 3 * 512 - 2),                      # y's 200 bytes reach x's next row
+    dict(y=F + 128, ldy=264), dict(y=F + 128, ldx=264),            # side by side, but rows at different distances
+    dict(out=6, y=F + 128, ldy=128),                               # fp32: 400 of 512 bytes
+    dict(y=2 * F + 200), dict(residual=4 * F + 198, ldr=256), dict(residual=4 * F + 314, ldr=256),
+    dict(bias=4 * F + 320), dict(T=1, y=F + 126), dict(T=1, y=2 * F + 120, ldw=256), dict(T=1, y=2 * F + 400, ldw=256),
+], ids=str)
+def test_linear_overlaps_are_refused(B, over):
+    _refused(B, _linear(B, **over))

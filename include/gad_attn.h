@@ -436,7 +436,9 @@ typedef enum {
  *             apart, written; values between the rows are left as they were
  *   T, K, N   1 to GAD_MAX_LINEAR each; row strides up to GAD_MAX_LINEAR_LD
  *
- * Sums and the epilogue are held in fp32, y is rounded once.  y may be the
+ * Sums and the epilogue are held in fp32, y is rounded once.  (The tensor cores cut
+ * a sum off at every 16 products.  At any K a fp32 result loses about 1e-6 of its
+ * terms' magnitudes by it, a 16-bit one up to 5e-5, a tenth of its rounding.)  y may be the
  * residual itself (same address and stride); any other overlap of y with the
  * inputs is refused (GAD_ERR_UNSUPPORTED).  Different columns of one wider matrix
  * (rows the same number of bytes apart) are no overlap; between rows at different

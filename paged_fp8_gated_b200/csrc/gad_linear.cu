@@ -190,8 +190,10 @@ int narrow_tokens(int T) {
     return ((T + tiles - 1) / tiles + 15) / 16 * 16;
 }
 
-// A chain of more than this many stages is promoted for a fp32 result.
-constexpr int kLongChain = 768 / gad::lin::BK;
+// A chain of more than this many stages is promoted: for a fp32 result, and for a
+// 16-bit one, whose rounding (2^-11 of it in fp16) hides up to 5e-5 from a chain of
+// 32,768 products, but not the 8e-4 that one of 524,288 loses.
+constexpr int kLongChain = 768 / gad::lin::BK, kLongChain16 = 32768 / gad::lin::BK;
 
 double larger(double a, double b) { return a > b ? a : b; }
 
@@ -217,7 +219,7 @@ double larger(double a, double b) { return a > b ? a : b; }
 //     fp32 41 and 43, 4,096 x 8,192 x 14,336 980 and 898).
 Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
     using namespace gad::lin;
-    const int nk = (K + BK - 1) / BK;
+    const int nk = (K + BK - 1) / BK, longest = f32 ? kLongChain : kLongChain16;
     Plan best;
     auto take = [&](const Plan& q) {
         if (q.us < best.us) best = q;
@@ -229,7 +231,7 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
         const long long tiles = static_cast<long long>((T + tt - 1) / tt) * ((N + ROWS - 1) / ROWS);
         for (int k = 0; k < kSplits && (1 << k) <= nk; ++k) {
             const int c = 1 << k, own = (nk + c - 1) / c;
-            const bool promote = f32 && own > kLongChain;
+            const bool promote = own > longest;
             for (int m = 0; m < kClasses; ++m) {
                 const int budget = smem_share(512 >> m);
                 if (narrow_cols(tt) * (promote ? 2 : 1) > 512 >> m || narrow_smem(tt, 1) > budget) continue;
@@ -262,7 +264,7 @@ Plan choose(int T, int K, int N, bool f32, const Capacity& cap, int sms) {
         const long long tiles = static_cast<long long>((T + 255) / 256) * ((N + bn - 1) / bn);
         for (int k = 0; k < 3 && (1 << k) <= nk; ++k) {
             const int own = (nk + (1 << k) - 1) >> k;
-            const bool promote = f32 && own > kLongChain;
+            const bool promote = own > longest;
             if (promote && bn != 128) continue;
             if (bn == 256 && k == 2) continue;            // always behind 128 (512 x 8,192 x 1,024 19.3, 18.2)
             if (k > 0 && tiles > cap.wide[k]) continue;   // a second wave of clusters costs more than it saves

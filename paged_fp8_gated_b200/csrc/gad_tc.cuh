@@ -68,19 +68,23 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Limits of the bounded waits.  A pipeline wait gives up after WAIT_LIMIT_NS;
-// the last waits of a kernel (for its own tensor-core operations and copies in
-// flight, before it frees tensor memory and exits) use TEARDOWN_LIMIT_NS.
+// Limits of the bounded waits.  There are two kinds, told apart by the type of the
+// limit that a call is given: a pipeline wait (no limit given) gives up after
+// WAIT_LIMIT_NS; the last waits of a kernel, for its own tensor-core operations and
+// copies in flight before it frees tensor memory and exits, are given
+// TEARDOWN_LIMIT_NS.
+struct LastWait {
+    unsigned long long limit_ns;
+};
 constexpr unsigned long long WAIT_LIMIT_NS = 2000000000ull;
-constexpr unsigned long long TEARDOWN_LIMIT_NS = 2000000001ull;
-// (The build that gives up at the first miss tells the two by their values: a block
-// that left with copies or MMAs in flight could fault.)
-static_assert(TEARDOWN_LIMIT_NS != WAIT_LIMIT_NS, "the last waits are waited for in every build");
+constexpr LastWait TEARDOWN_LIMIT_NS{2000000000ull};
 
 // The library built for the tests of the give-up path (and only that build)
 // defines GAD_TEST_GIVE_UP_AT_FIRST_MISS: there a pipeline wait whose phase has
 // not completed at its first, non-blocking probe gives up at once, so every
-// kernel with such a wait takes its give-up path on every run.
+// kernel with such a wait takes its give-up path on every run.  The last waits are
+// waited for in every build: a block that left with copies or MMAs in flight could
+// fault.
 #ifdef GAD_TEST_GIVE_UP_AT_FIRST_MISS
 constexpr bool kGiveUpAtFirstMiss = true;
 #else
@@ -90,14 +94,8 @@ constexpr bool kGiveUpAtFirstMiss = false;
 // Wait for phase `parity` of `bar`, giving up after `limit` ns (raising the
 // abort flag), or as soon as another thread has raised it if stop_on_abort.
 // Returns false on giving up.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                             bool stop_on_abort = true,
-                                             unsigned long long limit = WAIT_LIMIT_NS) {
-    if (kGiveUpAtFirstMiss && limit == WAIT_LIMIT_NS) {
-        if (mbar_test_wait(bar, parity)) return true;
-        *abort_flag = 1;
-        return false;
-    }
+__device__ __forceinline__ bool wait_until(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           bool stop_on_abort, unsigned long long limit) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
@@ -108,6 +106,20 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
             return false;
         }
     }
+}
+// A pipeline wait.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (kGiveUpAtFirstMiss) {
+        if (mbar_test_wait(bar, parity)) return true;
+        *abort_flag = 1;
+        return false;
+    }
+    return wait_until(bar, parity, abort_flag, true, WAIT_LIMIT_NS);
+}
+// A last wait.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             bool stop_on_abort, LastWait last) {
+    return wait_until(bar, parity, abort_flag, stop_on_abort, last.limit_ns);
 }
 
 __device__ __forceinline__ void fence_proxy_async_smem() {

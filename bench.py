@@ -49,8 +49,8 @@ FALLBACK_TC_TFLOPS = 1590.0  # dense bf16/fp16 burst
 # the hash of that kernel's sources when the counters were taken (null once the
 # sources change).
 TRAFFIC = {("decode32_full", "834f05e301e35d17"): 474125824,
-           ("verify16_full", "9ca1bf9de76aa245"): 336751104,
-           ("prefill1_full", "058148e4268a2ce9"): 22659328}
+           ("verify16_full", "671c1721f804c3eb"): 336929792,
+           ("prefill1_full", "4ef6b5dddd9e2394"): 22620416}
 
 # Sources of the step's main kernel: decode_kernel for single-token steps,
 # verify_tc_kernel for verify blocks, prefill_tc_kernel for longer blocks (the

@@ -437,7 +437,7 @@ typedef enum {
  *   T, K, N   1 to GAD_MAX_LINEAR each; row strides up to GAD_MAX_LINEAR_LD
  *
  * Sums and the epilogue are held in fp32, y is rounded once.  (The tensor cores cut
- * a sum off at every 16 products.  At any K a fp32 result loses about 1e-6 of its
+ * a sum off at every 16 products.  At any K a fp32 result loses up to 3e-6 of its
  * terms' magnitudes by it, a 16-bit one up to 5e-5, a tenth of its rounding.)  y may be the
  * residual itself (same address and stride); any other overlap of y with the
  * inputs is refused (GAD_ERR_UNSUPPORTED).  Different columns of one wider matrix
@@ -529,6 +529,15 @@ size_t gad_beam_workspace_bytes(int G, int W, int V, int K);
  * follow from the inputs alone.  Page ids outside [0, num_pages) are never
  * followed.  page_size is 1 or 64, rows 1 to GAD_MAX_B.
  *
+ * Between calls the caller may set an empty row's length to 0 (a new request) and
+ * else changes table and lengths only in step with refs.  To shorten a row (tokens
+ * of a verify block that were not accepted) first release the pages behind its new
+ * end, ceil(new / page_size) .. ceil(old / page_size) - 1: listed as a row of a table
+ * of their own, of as many full pages, they are freed by gad_pages_free; then lower
+ * lens[r].  Lowering it alone loses those pages to the pool: their counts stay, and
+ * the next extend overwrites their entries.  The new end must not lie inside a page
+ * that other rows share.
+ *
  * Calls run asynchronously on `stream`, allocate nothing and can be captured.  An
  * array that a call writes may not overlap another one of that call, the
  * workspace included (GAD_ERR_UNSUPPORTED).  The workspace (gad_pages_workspace_bytes, 256-byte aligned) needs no initial
@@ -591,7 +600,8 @@ int gad_pages_extend(int32_t* page_table, int32_t* lens, int rows, int L, int ma
 
 /*
  * Releases the pages of the rows r with leave[r] != 0 (uint8 [rows]; NULL:
- * all) and marks the rows empty (lens[r] = -1).
+ * all) and marks the rows empty (lens[r] = -1).  Table and lengths need not be
+ * those of the step: any rows of pages that are held can be released.
  */
 int gad_pages_free(const int32_t* page_table, int32_t* lens, int rows, const uint8_t* leave, int max_pages,
                    int page_size, int32_t* refs, int64_t num_pages, void* stream);

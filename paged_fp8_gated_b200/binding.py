@@ -652,7 +652,9 @@ def pages_workspace_bytes(rows: int, num_pages: int) -> int:
 
 def alloc_pages_workspace(rows: int, num_pages: int, device=None) -> torch.Tensor:
     """Scratch for the page operations on a pool of num_pages; its first word is
-    their status (step_status)."""
+    their status (step_status).  A call that is given no workspace takes one of its
+    own, whose status nobody can read: a pool without a page left then shows only in
+    what the call returns (extend: cache_loc -1; fork: shorter lens)."""
     return torch.empty(pages_workspace_bytes(rows, num_pages), dtype=torch.uint8, device=device or "cuda")
 
 
@@ -749,7 +751,17 @@ def pages_extend(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tenso
 def pages_free(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int,
                leave: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> None:
     """Releases the pages of the rows with leave[r] != 0 (uint8 or bool; None: all rows) and
-    marks them empty, through gad_pages_free; lens and refs are updated in place."""
+    marks them empty, through gad_pages_free; lens and refs are updated in place.
+
+    To shorten rows (tokens that were not accepted), release the pages behind their new
+    ends before lowering lens, as rows of a table of their own:
+
+        keep, had = -(-new // page_size), -(-lens // page_size)     # pages; new <= lens
+        tail = page_table.gather(1, (keep[:, None] + cols).clamp(0, page_table.shape[1] - 1).long())
+        pages_free(tail, (had - keep) * page_size, refs, page_size)
+        lens.copy_(new)
+
+    with cols = arange(the most pages that a row gives back)."""
     dev, rows, max_pages, num_pages = _pool(page_table, lens, refs)
     if leave is not None:
         _cuda(leave, "leave", dev, torch.bool if leave.dtype == torch.bool else torch.uint8, (rows,))

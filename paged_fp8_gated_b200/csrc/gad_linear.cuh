@@ -36,8 +36,9 @@
 // of four blocks than fit).
 //
 // Both can PROMOTE: the tensor cores cut the partial sum off at every step of
-// 16, so a chain of K products loses 1e-6 to 1.5e-6 of the result per 1,024
-// (measured).  Chains above 768 products for a fp32 result, and above 32,768 for a
+// 16, so a chain of K products loses 1.5e-6 of its terms' magnitudes per 1,024, and
+// up to 3e-6 at its start (measured on sums of positive terms; others lose a tenth).
+// Chains above 768 products for a fp32 result, and above 32,768 for a
 // 16-bit one (which rounds off ten times what such a chain loses), change
 // accumulators every 512 products, and warps that are idle otherwise add the
 // finished one up in registers, rounding to nearest.

@@ -38,10 +38,10 @@
 // Bound: one read of the logits; beside it one MUFU exponential per logit (16 a
 // cycle and SM: three quarters of the read's time for 16-bit logits) and about
 // four other instructions (maxima and sums in packed pairs).  Measured, both
-// kernels: 32 x 8 beams over 131,072 bf16 logits, K = 16, 20.8 us with the logits
-// in L2 and 23 from memory (a read at the copy rate 10.2, the exponentials 7.5,
+// kernels: 32 x 8 beams over 131,072 bf16 logits, K = 16, 21.1 us with the logits
+// in L2 and 23.5 from memory (a read at the copy rate 10.2, the exponentials 7.5,
 // about 8 the segment's end: threshold, second look, ranks, merge); 16 x 4 over
-// 32,001 fp32 10.3, 1 x 4 over 32,000 7.9, all latency.  Asking for lines ahead of
+// 32,001 fp32 10.6, 1 x 4 over 32,000 8.3, all latency.  Asking for lines ahead of
 // their load into L2 gained 1.3 us from memory and lost 1.2 from L2, where a product
 // has just left them: not done.
 #pragma once

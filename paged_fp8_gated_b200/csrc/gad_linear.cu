@@ -6,7 +6,6 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
-
 #include "gad_host.h"
 #include "gad_linear.cuh"
 
@@ -38,7 +37,6 @@ int linear_status_word(int** out) {
     return GAD_OK;
 }
 
-// [rows, K] 16-bit matrix, rows ld apart, in boxes of 64 x box_rows.
 // Tiles of box_cols x box_rows of a matrix of 16-bit values, box_cols of them the
 // swizzle's width.
 int encode_tiles(CUtensorMap* map, const void* base, bool fp16, int cols, int rows, long long ld, int box_cols,
@@ -113,8 +111,8 @@ struct Capacity {
     int wide[3];
 };
 
-int cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned blocks_x, unsigned blocks_y, int threads,
-                   int smem, int cluster, cudaStream_t s) {
+void cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned blocks_x, unsigned blocks_y, int threads,
+                    int smem, int cluster, cudaStream_t s) {
     std::memset(cfg, 0, sizeof(*cfg));
     cfg->gridDim = dim3(blocks_x, blocks_y);
     cfg->blockDim = dim3(static_cast<unsigned>(threads));
@@ -127,7 +125,6 @@ int cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned 
     attr->val.clusterDim.z = 1;
     cfg->attrs = attr;
     cfg->numAttrs = 1;
-    return GAD_OK;
 }
 
 // Stands for the kernels in the question how many clusters fit: for a kernel that

@@ -29,8 +29,8 @@
 // its K range: each finishes BN / S of the columns, with the other pairs' partial
 // sums, which they copy into its shared memory (bulk copies move 15 bytes a clock
 // between an SM and the others of its cluster, loads 9.5).  Measured: 4,096 x
-// 8,192 x 14,336 620 us in bursts, 0.96 of the tensor cores' measured rate, 715
-// for seconds on end (the power limit); 4,096 x 256 x 32,000 69 us, 3.9 TB/s,
+// 8,192 x 14,336 620 us in bursts without bias and activation, 0.96 of the tensor
+// cores' measured rate, 715 for seconds on end (the power limit); 4,096 x 256 x 32,000 69 us, 3.9 TB/s,
 // where writing y is the bound; 512 x 8,192 x 2,304 27 us, of which 5 after the
 // last MMA, on 36 of 74 pairs (36 tiles of 128 columns would need more clusters
 // of four blocks than fit).
@@ -41,7 +41,8 @@
 // Chains above 768 products for a fp32 result, and above 32,768 for a
 // 16-bit one (which rounds off ten times what such a chain loses), change
 // accumulators every 512 products, and warps that are idle otherwise add the
-// finished one up in registers, rounding to nearest.
+// finished one up in registers, rounding to nearest.  (Of those kernels two spill:
+// linear_narrow_kernel with 64 sums a thread 52 bytes, with 128 20 bytes.)
 #pragma once
 
 #include <cuda.h>
@@ -602,9 +603,6 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
     }
 }
 
-}  // namespace lin
-
-namespace lin {
 // The block's share (1 / S of the tokens x 128 rows) of a narrow tile: the
 // cluster's partial sums, in rank order, and the epilogue.  Several items' loads
 // are in flight at a time: those from other blocks take about 500 cycles.

@@ -428,7 +428,8 @@ typedef enum {
  *   y[t][n] = act(sum_k x[t][k] w[n][k] + bias[n]) + residual[t][n]
  *
  *   x         [T, K] of `dtype` (GAD_DTYPE_BF16 or GAD_DTYPE_F16), row t at
- *             x + t * ldx; 16-byte aligned, ldx a multiple of 8 values, >= K
+ *             x + t * ldx; 16-byte aligned, ldx a multiple of 8 values, >= K (a K
+ *             that is none leaves room behind the rows, which is not read)
  *   w         [N, K] of `dtype`, row n at w + n * ldw, as x
  *   bias      [N] of `dtype`, or NULL
  *   residual  [T, N] of `out_dtype`, rows ldr >= N values apart, or NULL
@@ -540,10 +541,10 @@ size_t gad_beam_workspace_bytes(int G, int W, int V, int K);
  *
  * Calls run asynchronously on `stream`, allocate nothing and can be captured.  An
  * array that a call writes may not overlap another one of that call, the
- * workspace included (GAD_ERR_UNSUPPORTED).  The workspace (gad_pages_workspace_bytes, 256-byte aligned) needs no initial
- * contents; calls that overlap on the GPU, or that share a pool, must not run
- * at the same time.  Its first word is the call's status: GAD_STATUS_PAGES_*
- * bits, read with gad_attn_step_status.
+ * workspace included (GAD_ERR_UNSUPPORTED).  The workspace
+ * (gad_pages_workspace_bytes, 256-byte aligned) needs no initial contents; calls
+ * that share it or a pool must not run at the same time.  Its first word is the
+ * call's status: GAD_STATUS_PAGES_* bits, read with gad_attn_step_status.
  */
 size_t gad_pages_workspace_bytes(int rows, int64_t num_pages);
 

@@ -541,7 +541,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
     """act(x @ w^T + bias) + residual through gad_linear.
 
     x [T, K] and w [N, K] bf16 or fp16 (rows contiguous, a multiple of 8 values
-    apart); bias [N] of their type; residual and the result [T, N] of
+    apart, so with room behind them if K is no multiple of 8); bias [N] of their type; residual and the result [T, N] of
     ``out_dtype`` (that of x, or float32).  ``activation``: one of ACTIVATIONS.
     ``out`` may be the residual itself.
     """

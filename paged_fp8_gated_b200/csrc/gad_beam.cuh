@@ -13,13 +13,13 @@
 // joins the segments' sums into lse_w and ranks the W S K candidates
 // (beam_merge_kernel).  The scores that decide the order are held in 64 bits, and
 // all sums in 64 bits or two words of 32, but those of the at most 32 exponentials
-// that a thread adds up at a time: lse_w is as good as the exponentials, however long the row.  Those are of
-// fp32 differences d scaled by log2 e, each off by at most 2.5 2^-24 |d| (the
-// difference's rounding, the product's and the constant's) + 2^-22 (the function)
-// + 2^-24 (a product with it) of itself.  A thread's terms are relative to a reference that moves only when the
-// maximum passes it by FAR, so a term is scaled once for its own difference, once
-// for every FAR that the maximum rises behind it, and once to the segment's maximum.
-// With the weights p_v = exp(x_v - lse) the sum of p times the distance to the row's
+// that a thread adds up at a time: lse_w is as good as the exponentials, however
+// long the row.  Those are of fp32 differences d scaled by log2 e, each off by at
+// most 2.5 2^-24 |d| (the difference's rounding, the product's and the constant's) +
+// 2^-22 (the function) + 2^-24 (a product with it) of itself.  A thread's terms are
+// relative to a reference that moves only when the maximum passes it by FAR, so a
+// term is scaled once for its own difference, once for every FAR that the maximum
+// rises behind it, and once to the segment's maximum.  With the weights p_v = exp(x_v - lse) the sum of p times the distance to the row's
 // maximum is at most log V, so lse_w is off by at most
 //
 //   2^-24 (2.5 (log V + 2 FAR) + 5 (2 + log V / FAR) + 18),

@@ -30,19 +30,19 @@
 // sums, which they copy into its shared memory (bulk copies move 15 bytes a clock
 // between an SM and the others of its cluster, loads 9.5).  Measured: 4,096 x
 // 8,192 x 14,336 620 us in bursts without bias and activation, 0.96 of the tensor
-// cores' measured rate, 715 for seconds on end (the power limit); 4,096 x 256 x 32,000 69 us, 3.9 TB/s,
-// where writing y is the bound; 512 x 8,192 x 2,304 27 us, of which 5 after the
+// cores' measured rate, 715 for seconds on end (the power limit); 4,096 x 256 x
+// 32,000 69 us, 3.9 TB/s, where writing y is the bound; 512 x 8,192 x 2,304 27 us, of which 5 after the
 // last MMA, on 36 of 74 pairs (36 tiles of 128 columns would need more clusters
 // of four blocks than fit).
 //
 // Both can PROMOTE: the tensor cores cut the partial sum off at every step of
 // 16, so a chain of K products loses 1.5e-6 of its terms' magnitudes per 1,024, and
 // up to 3e-6 at its start (measured on sums of positive terms; others lose a tenth).
-// Chains above 768 products for a fp32 result, and above 32,768 for a
-// 16-bit one (which rounds off ten times what such a chain loses), change
-// accumulators every 512 products, and warps that are idle otherwise add the
-// finished one up in registers, rounding to nearest.  (Of those kernels two spill:
-// linear_narrow_kernel with 64 sums a thread 52 bytes, with 128 20 bytes.)
+// Chains above 768 products for a fp32 result, and above 32,768 for a 16-bit one
+// (which rounds off ten times what such a chain loses), change accumulators every
+// 512 products, and warps that are idle otherwise add the finished one up in
+// registers, rounding to nearest.  (Of those kernels two spill: linear_narrow_kernel
+// with 64 sums a thread 52 bytes, with 128 20 bytes.)
 #pragma once
 
 #include <cuda.h>
